@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgnf4.so")
 SOURCES = ["api.hip", "pack.hip", "route.hip", "gather.hip", "decode.hip", "tile.hip",
-           "glue.hip", "dgrad.hip", "validate.hip"]
+           "glue.hip", "dgrad.hip", "validate.hip", "int4.hip", "moe_layer.hip"]
 CEIL_SOURCES = ["ceilings.hip"]
 CEIL_LIB = os.path.join(PKG, "libgnf4_ceilings.so")
 ARCH = "gfx950"

@@ -134,10 +134,47 @@ int gnf4_last_hip_error(void) { return g_last_hip_error; }
 const char* gnf4_version(void) { return "0.1.0"; }
 
 static bool valid_dtype(int32_t d) { return d == GNF4_DTYPE_BF16 || d == GNF4_DTYPE_F32; }
-// scale kind of an MXFP4 stack inside gemm_common: E8M0 bytes, one per 32 codes
-constexpr int32_t kScaleE8M0 = 2;
+// scale kind of an MXFP4 stack: E8M0 bytes, one per 32 codes
+constexpr int32_t kScaleE8M0 = GNF4_SCALE_E8M0;
 static size_t dtype_bytes(int32_t d) {
   return d == GNF4_DTYPE_BF16 ? 2 : d == kScaleE8M0 ? 1 : 4;
+}
+
+static bool valid_int4_group(int32_t group, int64_t K) {
+  return (group == 32 || group == 64 || group == 128) && K > 0 && K % group == 0;
+}
+// rows of one int4 linear call: 64 per workgroup along the grid's y
+constexpr int64_t kInt4MaxRows = (int64_t)1 << 20;
+
+// What gnf4_moe_layer serves: the route/sort's limits, up to
+// kMoeLayerMaxTokens tokens.
+static bool moe_layer_served(int64_t T, int64_t E, int32_t top_k) {
+  return T >= 0 && T <= kMoeLayerMaxTokens && E >= 1 && E <= 1024 && top_k >= 1 && top_k <= 32;
+}
+
+// Workspace of gnf4_moe_layer: the route/sort's outputs and scratch, then the
+// activations between the two projections; byte offsets, 256-byte aligned.
+struct MoeLayerRegions {
+  size_t offsets, sorted, sizes, ids, num_groups, route, h_hi, h_lo, total;
+};
+static MoeLayerRegions moe_layer_regions(int64_t T, int64_t E, int32_t top_k, int64_t I) {
+  MoeLayerRegions r;
+  size_t at = 0;
+  const auto take = [&at](size_t bytes) {
+    const size_t off = at;
+    at += align256(bytes);
+    return off;
+  };
+  r.offsets = take((size_t)(E + 1) * 4);
+  r.sorted = take((size_t)T * top_k * 4);
+  r.sizes = take((size_t)E * 4);
+  r.ids = take((size_t)E * 4);
+  r.num_groups = take(4);
+  r.route = take(plan_route(T, E, top_k).ws_bytes);
+  r.h_hi = take((size_t)T * top_k * I * 2);
+  r.h_lo = take((size_t)T * top_k * I * 2);
+  r.total = at;
+  return r;
 }
 
 gnf4_status gnf4_pack(const void* w, int32_t w_dtype, int64_t E, int64_t N, int64_t K,
@@ -732,6 +769,140 @@ gnf4_status gnf4_grouped_gemm_ex(const uint16_t* x_sorted, const uint8_t* packed
   return gemm_common(x_sorted, packed, absmax, absmax_dtype, E, N, K, group_sizes,
                      group_expert_ids, G, M, y, workspace, workspace_bytes, path, split_k,
                      stream);
+}
+
+gnf4_status gnf4_int4_pack(const void* w, int32_t w_dtype, int64_t N, int64_t K, int32_t group,
+                           uint8_t* packed, void* scales, int32_t scale_dtype, uint8_t* zeros,
+                           void* stream) {
+  if (!w || !packed || !scales) return GNF4_ERR_INVALID_ARG;
+  if (!valid_int4_group(group, K) || N <= 0) return GNF4_ERR_INVALID_ARG;
+  if (!valid_dtype(w_dtype) || !valid_dtype(scale_dtype)) return GNF4_ERR_INVALID_ARG;
+  if (!aligned(w, 16) || !aligned(packed, 4) || !aligned(scales, dtype_bytes(scale_dtype)))
+    return GNF4_ERR_INVALID_ARG;
+  if (N > INT64_MAX / K) return GNF4_ERR_INVALID_ARG;
+  const void* ptrs[] = {w, packed, scales};
+  for (const void* p : ptrs)
+    if (!is_device_ptr(p)) return GNF4_ERR_NOT_DEVICE_PTR;
+  if (zeros && !is_device_ptr(zeros)) return GNF4_ERR_NOT_DEVICE_PTR;
+  Int4PackArgs a;
+  a.w = w;
+  a.w_bf16 = w_dtype == GNF4_DTYPE_BF16;
+  a.n_weights = N * K;
+  a.group = group;
+  a.packed = packed;
+  a.scales = scales;
+  a.scale_bf16 = scale_dtype == GNF4_DTYPE_BF16;
+  a.zeros = zeros;
+  const hipError_t e = launch_int4_pack(a, (hipStream_t)stream);
+  return e == hipSuccess ? GNF4_OK : hip_fail(e);
+}
+
+gnf4_status gnf4_int4_linear(const uint16_t* x, int64_t M, const uint8_t* packed,
+                             const void* scales, int32_t scale_dtype, const uint8_t* zeros,
+                             int32_t group, int64_t N, int64_t K, const uint16_t* bias,
+                             uint16_t* y, void* stream) {
+  if (!valid_int4_group(group, K) || N <= 0 || M < 0) return GNF4_ERR_INVALID_ARG;
+  if (!valid_dtype(scale_dtype)) return GNF4_ERR_INVALID_ARG;
+  if (M == 0) return GNF4_OK;
+  if (M > kInt4MaxRows || N >= ((int64_t)1 << 30) || K >= ((int64_t)1 << 30))
+    return GNF4_ERR_UNSUPPORTED;
+  if (!x || !packed || !scales || !y) return GNF4_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(packed, 16) || !aligned(scales, dtype_bytes(scale_dtype)) ||
+      !aligned(y, 2) || (bias && !aligned(bias, 2)))
+    return GNF4_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, packed, scales, y};
+  for (const void* p : ptrs)
+    if (!is_device_ptr(p)) return GNF4_ERR_NOT_DEVICE_PTR;
+  if ((zeros && !is_device_ptr(zeros)) || (bias && !is_device_ptr(bias)))
+    return GNF4_ERR_NOT_DEVICE_PTR;
+  Int4LinearArgs a;
+  a.x = x;
+  a.packed = packed;
+  a.scales = scales;
+  a.scale_bf16 = scale_dtype == GNF4_DTYPE_BF16;
+  a.zeros = zeros;
+  a.bias = bias;
+  a.y = y;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.group = group;
+  const hipError_t e = launch_int4_linear(a, (hipStream_t)stream);
+  return e == hipSuccess ? GNF4_OK : hip_fail(e);
+}
+
+size_t gnf4_moe_layer_workspace_size(int64_t T, int64_t E, int32_t top_k, int64_t I) {
+  if (!moe_layer_served(T, E, top_k) || T == 0 || I <= 0 || I >= ((int64_t)1 << 30)) return 0;
+  return moe_layer_regions(T, E, top_k, I).total;
+}
+
+gnf4_status gnf4_moe_layer(const float* logits, int64_t T, int64_t E, int32_t top_k,
+                           const uint16_t* x, const uint8_t* gate_up_packed,
+                           const void* gate_up_scales, const uint8_t* down_packed,
+                           const void* down_scales, int32_t scale_kind, int64_t H, int64_t I,
+                           const uint16_t* residual, uint16_t* out, int32_t* topk_ids,
+                           float* topk_w, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  if (T < 0 || E < 1 || top_k < 1 || top_k > E || H < kBlock || H % kBlock != 0 || I < kBlock ||
+      I % kBlock != 0)
+    return GNF4_ERR_INVALID_ARG;
+  if (!valid_dtype(scale_kind) && scale_kind != GNF4_SCALE_E8M0) return GNF4_ERR_INVALID_ARG;
+  if (!moe_layer_served(T, E, top_k)) return GNF4_ERR_UNSUPPORTED;
+  if (I * H >= ((int64_t)1 << 31) || E * 2 * I >= ((int64_t)1 << 31) ||
+      E * H >= ((int64_t)1 << 31))
+    return GNF4_ERR_UNSUPPORTED;
+  if (T == 0) return GNF4_OK;
+  const void* words[] = {logits, topk_ids, topk_w};
+  for (const void* p : words)
+    if (!p || !aligned(p, 4)) return GNF4_ERR_INVALID_ARG;
+  const void* vecs[] = {x, gate_up_packed, down_packed};
+  for (const void* p : vecs)
+    if (!p || !aligned(p, 16)) return GNF4_ERR_INVALID_ARG;
+  const void* scales[] = {gate_up_scales, down_scales};
+  for (const void* p : scales)
+    if (!p || !aligned(p, dtype_bytes(scale_kind))) return GNF4_ERR_INVALID_ARG;
+  if (!out || !aligned(out, 2) || (residual && !aligned(residual, 2)))
+    return GNF4_ERR_INVALID_ARG;
+  const MoeLayerRegions r = moe_layer_regions(T, E, top_k, I);
+  if (!workspace || workspace_bytes < r.total) return GNF4_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return GNF4_ERR_INVALID_ARG;
+  const void* ptrs[] = {logits, topk_ids, topk_w, x, gate_up_packed, down_packed,
+                        gate_up_scales, down_scales, out, workspace};
+  for (const void* p : ptrs)
+    if (!is_device_ptr(p)) return GNF4_ERR_NOT_DEVICE_PTR;
+  if (residual && !is_device_ptr(residual)) return GNF4_ERR_NOT_DEVICE_PTR;
+
+  char* ws = static_cast<char*>(workspace);
+  const auto i32 = [ws](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
+  const RoutePlan plan = plan_route(T, E, top_k);
+  hipError_t e = launch_route_sort(logits, (int)T, (int)E, top_k, topk_ids, topk_w,
+                                   i32(r.offsets), i32(r.sorted), nullptr, i32(r.sizes),
+                                   i32(r.ids), i32(r.num_groups), i32(r.route), plan,
+                                   (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e);
+  MoeLayerArgs a;
+  a.x = x;
+  a.gu_packed = gate_up_packed;
+  a.gu_scales = gate_up_scales;
+  a.dn_packed = down_packed;
+  a.dn_scales = down_scales;
+  a.residual = residual;
+  a.out = out;
+  a.topk_w = topk_w;
+  a.offsets = i32(r.offsets);
+  a.sorted = i32(r.sorted);
+  a.group_sizes = i32(r.sizes);
+  a.group_ids = i32(r.ids);
+  a.num_groups = i32(r.num_groups);
+  a.h_hi = reinterpret_cast<uint16_t*>(ws + r.h_hi);
+  a.h_lo = reinterpret_cast<uint16_t*>(ws + r.h_lo);
+  a.T = (int)T;
+  a.E = (int)E;
+  a.top_k = top_k;
+  a.H = (int)H;
+  a.I = (int)I;
+  e = launch_moe_layer(a, scale_kind, (hipStream_t)stream);
+  return e == hipSuccess ? GNF4_OK : hip_fail(e);
 }
 
 }  // extern "C"

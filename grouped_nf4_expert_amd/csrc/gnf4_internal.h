@@ -322,6 +322,55 @@ hipError_t launch_combine(const uint16_t* y, const int32_t* slot_rows, const flo
                           int64_t T, int top_k, int64_t M, int64_t H, uint16_t* out,
                           hipStream_t stream);
 
+// int4 packing of n_weights = rows x K weights (int4.hip).
+struct Int4PackArgs {
+  const void* w;   // bf16 bits or fp32
+  bool w_bf16;
+  int64_t n_weights;
+  int group;       // 32, 64 or 128 weights per scale
+  uint8_t* packed;
+  void* scales;    // fp32 or bf16 bits
+  bool scale_bf16;
+  uint8_t* zeros;  // NULL: symmetric
+};
+hipError_t launch_int4_pack(const Int4PackArgs& a, hipStream_t stream);
+
+// y [M, N] = x [M, K] . dequant(W [N, K])^T + bias (int4.hip).
+struct Int4LinearArgs {
+  const uint16_t* x;
+  const uint8_t* packed;
+  const void* scales;
+  bool scale_bf16;
+  const uint8_t* zeros;    // NULL: every zero point is 8
+  const uint16_t* bias;    // NULL: none
+  uint16_t* y;
+  int M, N, K, group;
+};
+hipError_t launch_int4_linear(const Int4LinearArgs& a, hipStream_t stream);
+
+// A whole expert layer for a few tokens (moe_layer.hip), from the outputs of
+// launch_route_sort.
+constexpr int kMoeLayerMaxTokens = 64;
+struct MoeLayerArgs {
+  const uint16_t* x;          // [T, H]
+  const uint8_t* gu_packed;   // [E, 2I, H/2]
+  const void* gu_scales;
+  const uint8_t* dn_packed;   // [E, H, I/2]
+  const void* dn_scales;
+  const uint16_t* residual;   // [T, H] or NULL
+  uint16_t* out;              // [T, H]
+  const float* topk_w;        // [T, top_k]
+  const int32_t* offsets;     // [E + 1]
+  const int32_t* sorted;      // [T * top_k]
+  const int32_t* group_sizes;
+  const int32_t* group_ids;
+  const int32_t* num_groups;
+  uint16_t* h_hi;             // [T * top_k, I]: routing weight x SwiGLU as hi + lo
+  uint16_t* h_lo;
+  int T, E, top_k, H, I;
+};
+hipError_t launch_moe_layer(const MoeLayerArgs& a, int scale_kind, hipStream_t stream);
+
 int device_cu_count();
 
 // Opt-in check of device-resident grouping inputs (validate.hip).

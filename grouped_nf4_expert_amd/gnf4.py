@@ -19,8 +19,11 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgnf4.so")
 
 GNF4_OK = 0
+GNF4_ERR_NOT_DEVICE_PTR = 2
 GNF4_DTYPE_BF16 = 0
 GNF4_DTYPE_F32 = 1
+GNF4_SCALE_E8M0 = 2
+_GNF4_DTYPES = {torch.bfloat16: GNF4_DTYPE_BF16, torch.float32: GNF4_DTYPE_F32}
 PATH_AUTO, PATH_DECODE, PATH_TILE = 0, 1, 2
 
 _lib = None
@@ -110,6 +113,15 @@ def library():
     lib.gnf4_grouped_gemm_gather_noalloc.restype = ctypes.c_int
     lib.gnf4_grouped_gemm_gather_noalloc.argtypes = [vp, i64, vp, i32, vp, vp, i64, i64, i64, vp,
                                                      vp, i64, i64, vp, i32, i32, i32, vp]
+    lib.gnf4_int4_pack.restype = ctypes.c_int
+    lib.gnf4_int4_pack.argtypes = [vp, i32, i64, i64, i32, vp, vp, i32, vp, vp]
+    lib.gnf4_int4_linear.restype = ctypes.c_int
+    lib.gnf4_int4_linear.argtypes = [vp, i64, vp, vp, i32, vp, i32, i64, i64, vp, vp, vp]
+    lib.gnf4_moe_layer_workspace_size.restype = sz
+    lib.gnf4_moe_layer_workspace_size.argtypes = [i64, i64, i32, i64]
+    lib.gnf4_moe_layer.restype = ctypes.c_int
+    lib.gnf4_moe_layer.argtypes = [vp, i64, i64, i32, vp, vp, vp, vp, vp, i32, i64, i64, vp, vp,
+                                   vp, vp, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -136,6 +148,17 @@ def _need(t, name, dtype, ndim=None):
         raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _same_device(first, **others):
+    """Refuse host tensors and tensors that are not on `first`'s device (None
+    is skipped); return a context in which that device is the current one."""
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+    if not first.is_cuda:
+        raise Gnf4Error(GNF4_ERR_NOT_DEVICE_PTR, "host tensor")
+    return torch.cuda.device(first.device)
 
 
 # ------------------------------------------------------------------- pack
@@ -315,6 +338,144 @@ def moe_ffn_one_token(logits, x, gate_up, down, top_k, buffers=None, h=None, y=N
         _ptr(r.num_groups), _ptr(workspace), workspace.numel(), _stream()),
         "gnf4_moe_ffn_one_token")
     return y, h, r
+
+
+# -------------------------------------------------------------- moe_layer
+
+class MoeLayerBuffers:
+    """Preallocated outputs and workspace for repeated moe_layer calls of up
+    to ``T`` tokens on one stream."""
+
+    def __init__(self, T, E, top_k, H, I, device):
+        self.T, self.E, self.top_k, self.H, self.I = T, E, top_k, H, I
+        self.out = torch.empty((T, H), dtype=torch.bfloat16, device=device)
+        self.topk_ids = torch.empty((T, top_k), dtype=torch.int32, device=device)
+        self.topk_w = torch.empty((T, top_k), dtype=torch.float32, device=device)
+        self.ws_bytes = library().gnf4_moe_layer_workspace_size(T, E, top_k, I)
+        self.workspace = torch.empty(max(self.ws_bytes, 1), dtype=torch.uint8, device=device)
+
+
+def _scale_kind(scales):
+    return GNF4_SCALE_E8M0 if scales.dtype == torch.uint8 else _absmax_dtype(scales)
+
+
+def moe_layer(logits, x, gate_up, down, top_k, residual=None, buffers=None):
+    """A whole mixture-of-experts layer for 1 to 64 tokens: router top-k and
+    softmax over ``logits`` [T, E] fp32, gate_up, SwiGLU, down, and the
+    weighted sum over each token's experts, plus ``residual`` [T, H] if given.
+
+    ``x`` [T, H] bf16.  ``gate_up`` = (packed [E, 2I, H/2], scales) with the
+    gate rows first and ``down`` = (packed [E, H, I/2], scales): NF4 stacks
+    (scales = absmax, fp32 or bf16, per 64) or MXFP4 stacks (uint8 E8M0 per
+    32).  Returns (out [T, H] bf16, topk_ids [T, top_k], topk_w [T, top_k]):
+    ``buffers``' own tensors (their first T rows) where given."""
+    gp, gs = gate_up
+    dp, ds = down
+    _need(logits, "logits", torch.float32, 2)
+    _need(x, "x", torch.bfloat16, 2)
+    _need(gp, "gate_up packed", torch.uint8, 3)
+    _need(dp, "down packed", torch.uint8, 3)
+    _need(gs, "gate_up scales", gs.dtype, 3)
+    _need(ds, "down scales", gs.dtype, 3)
+    kind = _scale_kind(gs)
+    block = 32 if kind == GNF4_SCALE_E8M0 else 64
+    T, E = logits.shape
+    H, I = x.shape[1], gp.shape[1] // 2
+    if x.shape[0] != T:
+        raise ValueError("logits and x must have one row per token")
+    if gp.shape != (E, 2 * I, H // 2) or gs.shape != (E, 2 * I, H // block):
+        raise ValueError("gate_up must be [E, 2I, H/2] with scales per block")
+    if dp.shape != (E, H, I // 2) or ds.shape != (E, H, I // block):
+        raise ValueError("down must be [E, H, I/2] with scales per block")
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, 2)
+        if residual.shape != x.shape:
+            raise ValueError("residual must have x's shape")
+    with _same_device(x, logits=logits, gate_up=gp, gate_up_scales=gs, down=dp, down_scales=ds,
+                      residual=residual):
+        if buffers is None:
+            buffers = MoeLayerBuffers(T, E, top_k, H, I, x.device)
+        elif (T > buffers.T or (E, top_k, H, I) !=
+              (buffers.E, buffers.top_k, buffers.H, buffers.I)):
+            raise ValueError("buffers were made for another layer or for fewer tokens")
+        b = buffers
+        if b.workspace.device != x.device:
+            raise ValueError(f"buffers are on {b.workspace.device}, expected {x.device}")
+        _check(library().gnf4_moe_layer(
+            _ptr(logits), T, E, top_k, _ptr(x), _ptr(gp), _ptr(gs), _ptr(dp), _ptr(ds), kind, H,
+            I, _ptr(residual), _ptr(b.out), _ptr(b.topk_ids), _ptr(b.topk_w), _ptr(b.workspace),
+            b.ws_bytes, _stream()), "gnf4_moe_layer")
+    if T == b.T:
+        return b.out, b.topk_ids, b.topk_w
+    return b.out[:T], b.topk_ids[:T], b.topk_w[:T]
+
+
+# ------------------------------------------------------------------- int4
+
+def int4_pack(w, group=128, zero_points=False, scale_dtype=torch.bfloat16):
+    """int4 codes of ``w`` [..., N, K] (bf16 or fp32 on the GPU) with one scale
+    per ``group`` (32, 64 or 128) weights along K.
+
+    Returns ``(packed uint8 [..., N, K/2], scales [..., N, K/group], zeros)``;
+    ``zeros`` is None for symmetric codes, else uint8 [..., N, K/group].  A
+    weight reads back as (code - zero) * scale, symmetric zeros being 8."""
+    if w.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("w must be bfloat16 or float32")
+    _need(w, "w", w.dtype)
+    if w.dim() < 2:
+        raise ValueError("w must be at least 2-D")
+    if group not in (32, 64, 128) or w.shape[-1] % group:
+        raise ValueError("group must be 32, 64 or 128 and divide K")
+    sdt = _GNF4_DTYPES.get(scale_dtype)
+    if sdt is None:
+        raise TypeError("scale_dtype must be float32 or bfloat16")
+    K = w.shape[-1]
+    rows = w.numel() // max(K, 1)
+    with _same_device(w):
+        packed = torch.empty(w.shape[:-1] + (K // 2,), dtype=torch.uint8, device=w.device)
+        scales = torch.empty(w.shape[:-1] + (K // group,), dtype=scale_dtype, device=w.device)
+        zeros = None
+        if zero_points:
+            zeros = torch.empty(scales.shape, dtype=torch.uint8, device=w.device)
+        _check(library().gnf4_int4_pack(_ptr(w), _GNF4_DTYPES[w.dtype], rows, K, group,
+                                        _ptr(packed), _ptr(scales), sdt, _ptr(zeros), _stream()),
+               "gnf4_int4_pack")
+    return packed, scales, zeros
+
+
+def int4_linear(x, packed, scales, zeros=None, bias=None, out=None):
+    """y[M, N] (bf16) = x [M, K] @ dequant(W [N, K])^T + bias over weights as
+    int4_pack returns them (the group is K / scales.shape[1])."""
+    _need(x, "x", torch.bfloat16, 2)
+    _need(packed, "packed", torch.uint8, 2)
+    _need(scales, "scales", scales.dtype, 2)
+    sdt = _GNF4_DTYPES.get(scales.dtype)
+    if sdt is None:
+        raise TypeError("scales must be float32 or bfloat16")
+    M, K = x.shape
+    N, half_k = packed.shape
+    groups = scales.shape[1]
+    if 2 * half_k != K or scales.shape[0] != N or groups == 0 or K % groups:
+        raise ValueError("x/packed/scales shapes do not agree")
+    if zeros is not None:
+        _need(zeros, "zeros", torch.uint8, 2)
+        if zeros.shape != scales.shape:
+            raise ValueError("zeros must have the scales' shape")
+    if bias is not None:
+        _need(bias, "bias", torch.bfloat16, 1)
+        if bias.shape[0] != N:
+            raise ValueError("bias must hold N entries")
+    if out is not None:
+        _need(out, "out", torch.bfloat16, 2)
+        if out.shape != (M, N):
+            raise ValueError("out must be [M, N]")
+    with _same_device(x, packed=packed, scales=scales, zeros=zeros, bias=bias, out=out):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        _check(library().gnf4_int4_linear(_ptr(x), M, _ptr(packed), _ptr(scales), sdt,
+                                          _ptr(zeros), K // groups, N, K, _ptr(bias), _ptr(out),
+                                          _stream()), "gnf4_int4_linear")
+    return out
 
 
 # ------------------------------------------------------------------ MXFP4

@@ -67,6 +67,10 @@ typedef enum gnf4_dtype {
   GNF4_DTYPE_F32 = 1
 } gnf4_dtype;
 
+/* Scale kind of an MXFP4 stack, where a call takes one beside the dtypes:
+ * E8M0 bytes, one per 32 codes. */
+#define GNF4_SCALE_E8M0 2
+
 /* Human-readable text for a status code (static storage). */
 const char* gnf4_status_string(gnf4_status s);
 
@@ -263,6 +267,111 @@ gnf4_status gnf4_moe_ffn_one_token(const float* logits, int64_t E, int32_t top_k
                                    int32_t* slot_rows, int32_t* group_sizes,
                                    int32_t* group_expert_ids, int32_t* num_groups,
                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gnf4_moe_layer -- a whole mixture-of-experts layer for a few tokens:
+ *   ids, w  = the top_k experts of each token and their softmax weights, as
+ *             gnf4_route_sort writes them
+ *   h[t, j] = w[t, j] * silu(x[t] . Wg[ids[t, j]]^T) * (x[t] . Wu[ids[t, j]]^T)
+ *   out[t]  = residual[t] + sum_j h[t, j] . Wd[ids[t, j]]^T
+ * with every sum in fp32 and one rounding to bf16 at the end (h travels
+ * between the two projections as the sum of two bf16 numbers).
+ *
+ * Landing page "grouped-nf4-gemm": "Owns" (the grouped packed GEMM over NF4
+ * and native MXFP4, the router, swiglu and combine glue) and "Use this when"
+ * (a decode step's small operations in as few launches as possible).  Beside
+ * gnf4_moe_ffn_one_token it takes up to 64 tokens, any layer shape, both
+ * formats, and ends with the combine.  The experts' weights are read once for
+ * all of their tokens.
+ *
+ *   logits            [T, E] fp32 router logits (finite)
+ *   x                 [T, H] bf16 bits, 16-byte aligned
+ *   gate_up_packed    [E, 2I, H/2] uint8, gate rows first (16-byte aligned)
+ *   down_packed       [E, H, I/2] uint8 (16-byte aligned)
+ *   gate_up_scales, down_scales, scale_kind:
+ *     GNF4_DTYPE_F32 or GNF4_DTYPE_BF16: an NF4 stack as gnf4_pack_ex writes
+ *       it, scales = absmax [E, rows, K/64]
+ *     GNF4_SCALE_E8M0: an MXFP4 stack as gnf4_grouped_gemm_mxfp4 takes it,
+ *       scales [E, rows, K/32] uint8
+ *   residual          [T, H] bf16 bits, optional (NULL: none); may be x, may
+ *                     be out
+ *   out               [T, H] bf16 bits out
+ *   topk_ids, topk_w  [T, top_k] int32 and fp32 out
+ *   workspace         device scratch of gnf4_moe_layer_workspace_size() bytes
+ *                     (16-byte aligned; nothing in it needs to be set or is
+ *                     kept between calls; calls that may overlap need one each)
+ *
+ * Experts no token picked are not read.  Scales must be finite (an E8M0 0xFF
+ * is NaN and gives NaN in the outputs it reaches).  Deterministic.
+ * Limits: 0 <= T <= 64, 1 <= E <= 1024, 1 <= top_k <= min(E, 32), H and I
+ * positive multiples of 64, I * H, E * 2I and E * H below 2^31.
+ * Errors: GNF4_ERR_INVALID_ARG, GNF4_ERR_UNSUPPORTED (a size above the
+ * limits), GNF4_ERR_NOT_DEVICE_PTR, GNF4_ERR_WORKSPACE, GNF4_ERR_HIP.
+ */
+size_t gnf4_moe_layer_workspace_size(int64_t T, int64_t E, int32_t top_k, int64_t I);
+
+gnf4_status gnf4_moe_layer(const float* logits, int64_t T, int64_t E, int32_t top_k,
+                           const uint16_t* x, const uint8_t* gate_up_packed,
+                           const void* gate_up_scales, const uint8_t* down_packed,
+                           const void* down_scales, int32_t scale_kind, int64_t H, int64_t I,
+                           const uint16_t* residual, uint16_t* out, int32_t* topk_ids,
+                           float* topk_w, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gnf4_int4_pack -- int4 codes of a weight matrix with one scale, and if
+ * asked one zero point, per group of weights along K.
+ *
+ * Landing page "grouped-nf4-gemm", "Owns" (the int4 GEMV and its packer, the
+ * format of a served model's dense projections).
+ *
+ *   w       [N, K] of `w_dtype` (bf16 bits or fp32), 16-byte aligned, finite;
+ *           a stack [E, N, K] is E * N rows
+ *   group   32, 64 or 128 weights of a row per scale; K a multiple of it
+ *   packed  [N, K/2] uint8 out: byte j of a row = (code[2j] << 4) | code[2j+1]
+ *           (the first element in the high nibble, as gnf4_pack), 4-byte aligned
+ *   scales  [N, K/group] out, `scale_dtype` (fp32, or bf16 bits)
+ *   zeros   [N, K/group] uint8 out, or NULL for symmetric codes
+ *
+ * A weight is read back as (code - z) * s.  Symmetric: s = max |w| / 7 and
+ * z = 8.  With zeros: lo = max(-w, 0) and hi = max(w, 0) over the group,
+ * s = hi / 15 + lo / 15, z = the whole number in [0, 15] nearest to lo / s.
+ * Quotients and the sum are rounded to fp32, then s to its stored type; codes
+ * and zero points follow from the stored s: the code is the level nearest to w
+ * in exact arithmetic, ties to the lower one (as gnf4_pack).  A group with
+ * s == 0 stores its zero point (z = 0 with zeros) everywhere.
+ * Errors: GNF4_ERR_INVALID_ARG (null pointer, N/K <= 0, a group other than
+ * these, K % group != 0, bad dtype, misalignment), GNF4_ERR_NOT_DEVICE_PTR,
+ * GNF4_ERR_HIP.
+ */
+gnf4_status gnf4_int4_pack(const void* w, int32_t w_dtype, int64_t N, int64_t K, int32_t group,
+                           uint8_t* packed, void* scales, int32_t scale_dtype, uint8_t* zeros,
+                           void* stream);
+
+/*
+ * gnf4_int4_linear -- y[m, n] = sum_k x[m, k] (code[n, k] - z[n, k/group])
+ * s[n, k/group] + bias[n] over weights as gnf4_int4_pack writes them.
+ *
+ * Landing page "grouped-nf4-gemm", "Owns" (the int4 GEMV for a decode step's
+ * dense projections beside the experts).
+ *
+ *   x       [M, K] bf16 bits, 16-byte aligned
+ *   packed  [N, K/2] uint8, 16-byte aligned
+ *   scales  [N, K/group] fp32 or bf16 bits (`scale_dtype`)
+ *   zeros   [N, K/group] uint8 zero points 0..15, or NULL: every one is 8
+ *   bias    [N] bf16 bits, or NULL
+ *   y       [M, N] bf16 bits out
+ *
+ * Products of activations and codes are exact; a group's sum and the sums over
+ * groups are fp32, y is rounded once.  Any M (one row up to a prompt's chunk)
+ * and any N; the weights are read once per 64 rows.  Deterministic; a row's
+ * result does not depend on the other rows.
+ * Limits: M <= 2^20, N and K below 2^30.  Errors: GNF4_ERR_INVALID_ARG,
+ * GNF4_ERR_UNSUPPORTED, GNF4_ERR_NOT_DEVICE_PTR, GNF4_ERR_HIP.
+ */
+gnf4_status gnf4_int4_linear(const uint16_t* x, int64_t M, const uint8_t* packed,
+                             const void* scales, int32_t scale_dtype, const uint8_t* zeros,
+                             int32_t group, int64_t N, int64_t K, const uint16_t* bias,
+                             uint16_t* y, void* stream);
 
 /*
  * gnf4_gather_rows -- build the grouped activations from token rows:

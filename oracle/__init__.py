@@ -31,6 +31,8 @@ What the oracle computes, and the passage each step follows:
   scales per 32 elements), the second packed format the landing page's
   grouped GEMM serves ("Owns", "Use this when"); the formats' definitions
   come from the OCP Microscaling specification.
+* ``int4``  -- int4 codes with group scales and zero points, their packer and
+  the linear layer over them (landing page "Owns": the int4 GEMV and packer).
 * ``moe``   -- the steps on either side of the GEMM: the SwiGLU activation
   between the two expert projections and the weighted top-k combine after
   the down projection (landing page "grouped-nf4-gemm", "Owns" and "Use this
@@ -53,6 +55,7 @@ from .gemm import ref_group_rows, ref_grouped_gemm, ref_grouped_gemm_entries, re
 from .moe import ref_silu, ref_swiglu, ref_combine, ref_expert_projection, ref_moe_ffn
 from .mxfp4 import (E2M1_TABLE, ref_e2m1_value, ref_e8m0_value, ref_mx_codes, ref_mx_unpack,
                     ref_grouped_gemm_mxfp4)
+from .int4 import ref_int4_pack, ref_int4_unpack, ref_int4_linear
 
 __all__ = [
     "NF4_TABLE", "ref_pack", "ref_unpack", "ref_codes", "ref_quantize_block",
@@ -62,4 +65,5 @@ __all__ = [
     "ref_silu", "ref_swiglu", "ref_combine", "ref_expert_projection", "ref_moe_ffn",
     "E2M1_TABLE", "ref_e2m1_value", "ref_e8m0_value", "ref_mx_codes", "ref_mx_unpack",
     "ref_grouped_gemm_mxfp4",
+    "ref_int4_pack", "ref_int4_unpack", "ref_int4_linear",
 ]
