@@ -152,12 +152,12 @@ static bool moe_layer_served(int64_t T, int64_t E, int32_t top_k) {
   return T >= 0 && T <= kMoeLayerMaxTokens && E >= 1 && E <= 1024 && top_k >= 1 && top_k <= 32;
 }
 
-// Workspace of gnf4_moe_layer: the route/sort's outputs and scratch, then the
-// activations between the two projections; byte offsets, 256-byte aligned.
+// Workspace of gnf4_moe_layer: the entry list, the slots' rows and what the
+// launches hand on; byte offsets, 256-byte aligned.
 struct MoeLayerRegions {
-  size_t offsets, sorted, sizes, ids, num_groups, route, h_hi, h_lo, total;
+  size_t entries, slot_rows, h, y, total;
 };
-static MoeLayerRegions moe_layer_regions(int64_t T, int64_t E, int32_t top_k, int64_t I) {
+static MoeLayerRegions moe_layer_regions(int64_t T, int32_t top_k, int64_t H, int64_t I) {
   MoeLayerRegions r;
   size_t at = 0;
   const auto take = [&at](size_t bytes) {
@@ -165,14 +165,11 @@ static MoeLayerRegions moe_layer_regions(int64_t T, int64_t E, int32_t top_k, in
     at += align256(bytes);
     return off;
   };
-  r.offsets = take((size_t)(E + 1) * 4);
-  r.sorted = take((size_t)T * top_k * 4);
-  r.sizes = take((size_t)E * 4);
-  r.ids = take((size_t)E * 4);
-  r.num_groups = take(4);
-  r.route = take(plan_route(T, E, top_k).ws_bytes);
-  r.h_hi = take((size_t)T * top_k * I * 2);
-  r.h_lo = take((size_t)T * top_k * I * 2);
+  const size_t rows = (size_t)T * top_k;
+  r.entries = take((1 + kMoeLayerMaxEntries) * sizeof(uint32_t));
+  r.slot_rows = take(rows * sizeof(int32_t));
+  r.h = take(rows * I * sizeof(float));
+  r.y = take(rows * H * sizeof(float));
   r.total = at;
   return r;
 }
@@ -831,9 +828,11 @@ gnf4_status gnf4_int4_linear(const uint16_t* x, int64_t M, const uint8_t* packed
   return e == hipSuccess ? GNF4_OK : hip_fail(e);
 }
 
-size_t gnf4_moe_layer_workspace_size(int64_t T, int64_t E, int32_t top_k, int64_t I) {
-  if (!moe_layer_served(T, E, top_k) || T == 0 || I <= 0 || I >= ((int64_t)1 << 30)) return 0;
-  return moe_layer_regions(T, E, top_k, I).total;
+size_t gnf4_moe_layer_workspace_size(int64_t T, int64_t E, int32_t top_k, int64_t H, int64_t I) {
+  if (!moe_layer_served(T, E, top_k) || T == 0 || H <= 0 || I <= 0 ||
+      H > kMoeLayerMaxWidth || I > kMoeLayerMaxWidth)
+    return 0;
+  return moe_layer_regions(T, top_k, H, I).total;
 }
 
 gnf4_status gnf4_moe_layer(const float* logits, int64_t T, int64_t E, int32_t top_k,
@@ -848,9 +847,7 @@ gnf4_status gnf4_moe_layer(const float* logits, int64_t T, int64_t E, int32_t to
     return GNF4_ERR_INVALID_ARG;
   if (!valid_dtype(scale_kind) && scale_kind != GNF4_SCALE_E8M0) return GNF4_ERR_INVALID_ARG;
   if (!moe_layer_served(T, E, top_k)) return GNF4_ERR_UNSUPPORTED;
-  if (I * H >= ((int64_t)1 << 31) || E * 2 * I >= ((int64_t)1 << 31) ||
-      E * H >= ((int64_t)1 << 31))
-    return GNF4_ERR_UNSUPPORTED;
+  if (H > kMoeLayerMaxWidth || I > kMoeLayerMaxWidth) return GNF4_ERR_UNSUPPORTED;
   if (T == 0) return GNF4_OK;
   const void* words[] = {logits, topk_ids, topk_w};
   for (const void* p : words)
@@ -863,7 +860,7 @@ gnf4_status gnf4_moe_layer(const float* logits, int64_t T, int64_t E, int32_t to
     if (!p || !aligned(p, dtype_bytes(scale_kind))) return GNF4_ERR_INVALID_ARG;
   if (!out || !aligned(out, 2) || (residual && !aligned(residual, 2)))
     return GNF4_ERR_INVALID_ARG;
-  const MoeLayerRegions r = moe_layer_regions(T, E, top_k, I);
+  const MoeLayerRegions r = moe_layer_regions(T, top_k, H, I);
   if (!workspace || workspace_bytes < r.total) return GNF4_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return GNF4_ERR_INVALID_ARG;
   const void* ptrs[] = {logits, topk_ids, topk_w, x, gate_up_packed, down_packed,
@@ -873,14 +870,8 @@ gnf4_status gnf4_moe_layer(const float* logits, int64_t T, int64_t E, int32_t to
   if (residual && !is_device_ptr(residual)) return GNF4_ERR_NOT_DEVICE_PTR;
 
   char* ws = static_cast<char*>(workspace);
-  const auto i32 = [ws](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
-  const RoutePlan plan = plan_route(T, E, top_k);
-  hipError_t e = launch_route_sort(logits, (int)T, (int)E, top_k, topk_ids, topk_w,
-                                   i32(r.offsets), i32(r.sorted), nullptr, i32(r.sizes),
-                                   i32(r.ids), i32(r.num_groups), i32(r.route), plan,
-                                   (hipStream_t)stream);
-  if (e != hipSuccess) return hip_fail(e);
   MoeLayerArgs a;
+  a.logits = logits;
   a.x = x;
   a.gu_packed = gate_up_packed;
   a.gu_scales = gate_up_scales;
@@ -888,20 +879,18 @@ gnf4_status gnf4_moe_layer(const float* logits, int64_t T, int64_t E, int32_t to
   a.dn_scales = down_scales;
   a.residual = residual;
   a.out = out;
+  a.topk_ids = topk_ids;
   a.topk_w = topk_w;
-  a.offsets = i32(r.offsets);
-  a.sorted = i32(r.sorted);
-  a.group_sizes = i32(r.sizes);
-  a.group_ids = i32(r.ids);
-  a.num_groups = i32(r.num_groups);
-  a.h_hi = reinterpret_cast<uint16_t*>(ws + r.h_hi);
-  a.h_lo = reinterpret_cast<uint16_t*>(ws + r.h_lo);
+  a.entries = reinterpret_cast<uint32_t*>(ws + r.entries);
+  a.slot_rows = reinterpret_cast<int32_t*>(ws + r.slot_rows);
+  a.h = reinterpret_cast<float*>(ws + r.h);
+  a.y = reinterpret_cast<float*>(ws + r.y);
   a.T = (int)T;
   a.E = (int)E;
   a.top_k = top_k;
   a.H = (int)H;
   a.I = (int)I;
-  e = launch_moe_layer(a, scale_kind, (hipStream_t)stream);
+  const hipError_t e = launch_moe_layer(a, scale_kind, (hipStream_t)stream);
   return e == hipSuccess ? GNF4_OK : hip_fail(e);
 }
 

@@ -348,10 +348,15 @@ struct Int4LinearArgs {
 };
 hipError_t launch_int4_linear(const Int4LinearArgs& a, hipStream_t stream);
 
-// A whole expert layer for a few tokens (moe_layer.hip), from the outputs of
-// launch_route_sort.
+// A whole expert layer for a few tokens (moe_layer.hip).
 constexpr int kMoeLayerMaxTokens = 64;
+// entries (up to 16 routed rows of one expert) of the largest call: one per
+// expert, and one more for every 16 of its 64 x 32 rows
+constexpr int kMoeLayerMaxEntries = 1024 + kMoeLayerMaxTokens * 32 / 16;
+// widest H or I: eight wavefronts hold the activations of eight steps of 128 each
+constexpr int kMoeLayerMaxWidth = 8192;
 struct MoeLayerArgs {
+  const float* logits;        // [T, E]
   const uint16_t* x;          // [T, H]
   const uint8_t* gu_packed;   // [E, 2I, H/2]
   const void* gu_scales;
@@ -359,14 +364,12 @@ struct MoeLayerArgs {
   const void* dn_scales;
   const uint16_t* residual;   // [T, H] or NULL
   uint16_t* out;              // [T, H]
-  const float* topk_w;        // [T, top_k]
-  const int32_t* offsets;     // [E + 1]
-  const int32_t* sorted;      // [T * top_k]
-  const int32_t* group_sizes;
-  const int32_t* group_ids;
-  const int32_t* num_groups;
-  uint16_t* h_hi;             // [T * top_k, I]: routing weight x SwiGLU as hi + lo
-  uint16_t* h_lo;
+  int32_t* topk_ids;          // [T, top_k]
+  float* topk_w;              // [T, top_k]
+  uint32_t* entries;          // the number of entries, then the entries
+  int32_t* slot_rows;         // [T * top_k]: grouped row of each slot
+  float* h;                   // [T * top_k, I]: routing weight x SwiGLU
+  float* y;                   // [T * top_k, H]: the down projection's rows
   int T, E, top_k, H, I;
 };
 hipError_t launch_moe_layer(const MoeLayerArgs& a, int scale_kind, hipStream_t stream);

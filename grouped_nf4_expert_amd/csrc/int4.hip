@@ -134,7 +134,7 @@ __global__ __launch_bounds__(kLinWaves* kWave) void int4_linear_kernel(Int4Linea
     xrow[t] = a.x + (size_t)min(m0 + t * 16 + col, a.M - 1) * a.K;
   fill_lut<W4::kInt4>(lut);
   __syncthreads();
-  const uint32_t copy = lut_copy<W4::kInt4>(lane);
+  const uint32_t copy = lut_copy(lane);
   f32x4 acc[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -144,10 +144,10 @@ __global__ __launch_bounds__(kLinWaves* kWave) void int4_linear_kernel(Int4Linea
     load_step<B, ZP>(w, c, g, a.K, d);
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      bf16x8 x[1][4];
+      u32x4 x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[0][i] = load_frag(xrow[t], c * kStep + k_of<B>(g, i), a.K);
-      acc[t] = step_mac<W4::kInt4, B, ZP, 1>(d, x, lut, copy, acc[t]);
+      for (int i = 0; i < 4; ++i) x[i] = load_frag(xrow[t], c * kStep + k_of<B>(g, i), a.K);
+      acc[t] = step_mac_zp<B, ZP>(d, x, lut, copy, acc[t]);
     }
   }
 #pragma unroll

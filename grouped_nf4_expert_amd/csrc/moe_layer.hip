@@ -1,153 +1,697 @@
-// A whole mixture-of-experts layer for a few tokens.
+// A whole mixture-of-experts layer for a few tokens: three launches.
+//
+//  1. moe_gate_up_kernel: routing, gate_up and SwiGLU.  Every workgroup routes
+//     all tokens itself (a few thousand logits; a launch of its own would cost
+//     more than the work) and then takes its share of the work items;
+//  2. moe_down_kernel: the down projection, one fp32 row per routed slot;
+//  3. moe_sum_kernel: each token's sum over its slots, and the residual.
+//
+// Both projections share one shape (expert_tiles).  A work item is an entry --
+// up to 16 routed rows of one expert, one matrix-core tile -- and 32 weight
+// rows.  The eight wavefronts of a workgroup form teams; a team owns an item, its
+// wavefronts take every wk-th step of K and their sums meet in LDS.  One
+// workgroup per CU stays resident and each team walks a contiguous range of
+// items, so
+//  * the decode table and the routing are made once;
+//  * a wavefront always meets the same steps of K, and its activations (the
+//    entry's rows at those steps) stay in registers until the entry changes:
+//    read per item, they cost the address units four times what the weights
+//    do;
+//  * each wavefront loads weights ahead, across items and barriers: a CU must
+//    keep tens of kilobytes in flight to draw its share of the HBM stream.
 
+#include <math.h>
+
+#include "route_core.h"
 #include "w4_mfma.h"
 
 namespace gnf4 {
 namespace {
 
-constexpr int kGuWaves = 8;
-constexpr int kDnWaves = 16;
+constexpr int kWaves = 8;
+constexpr int kThreads = kWaves * kWave;
+// items of a group that shares the activations of a pass: gate_up's and down's
+// entries have multiples of 4 and of 2
+constexpr int kGuGroup = 2, kDnGroup = 2;
+constexpr int kMaxE = 1024;
+constexpr int kMaxRows = kMoeLayerMaxTokens * 32;  // top_k <= 32
+constexpr int kMaxEntries = kMoeLayerMaxEntries;
 
-// gate_up and SwiGLU.  Work item: one routed expert and 16 gate rows with
-// their 16 up rows; the wavefronts split K and their sums meet in LDS.  h is
-// scaled by the token's routing weight here, so the down projection's sums
-// over a token's experts need no further factor, and kept as a sum of two
-// bf16 numbers (hi + lo, within 2^-17): one rounding to bf16 would cost as
-// much accuracy as the layer's output rounding.
-template <W4 F, int B, typename S>
-__global__ __launch_bounds__(kGuWaves* kWave) void moe_gate_up_kernel(MoeLayerArgs a) {
-  __shared__ __align__(16) char lut[F == W4::kMx4 ? 16 : kLutBytes];
-  __shared__ float red[kGuWaves][2][256];
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  const int g = lane >> 4, col = lane & 15;
-  fill_lut<F>(lut);
-  __syncthreads();
-  const uint32_t copy = lut_copy<F>(lane);
-  const int tiles = a.I / 16;
-  const int items = a.num_groups[0] * tiles;
-  const int steps = (a.H + kStep - 1) / kStep;
-  const size_t kb = a.H / 2, blocks = a.H / B;
-  for (int it = blockIdx.x; it < items; it += gridDim.x) {
-    const int j = it / tiles, n0 = (it % tiles) * 16;
-    const int e = a.group_ids[j], cnt = a.group_sizes[j], off = a.offsets[e];
-    const size_t rg = (size_t)e * 2 * a.I + n0 + col, ru = rg + a.I;
-    const S* sc = static_cast<const S*>(a.gu_scales);
-    const WeightRow<S> wg = {a.gu_packed + rg * kb, sc + rg * blocks, nullptr};
-    const WeightRow<S> wu = {a.gu_packed + ru * kb, sc + ru * blocks, nullptr};
-    for (int r0 = 0; r0 < cnt; r0 += 16) {
-      const int slot = a.sorted[off + min(r0 + col, cnt - 1)];
-      const uint16_t* xrow = a.x + (size_t)(slot / a.top_k) * a.H;
-      f32x4 ag = {0.0f, 0.0f, 0.0f, 0.0f}, au = ag;
-      for (int c = wave; c < steps; c += kGuWaves) {
-        StepData<B, S> dg, du;
-        load_step<B, false>(wg, c, g, a.H, dg);
-        load_step<B, false>(wu, c, g, a.H, du);
-        bf16x8 x[1][4];
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// An entry: up to 16 grouped rows of one expert.
+__device__ __forceinline__ uint32_t make_entry(int e, int row0, int cnt) {
+  return (uint32_t)e | ((uint32_t)row0 << 10) | ((uint32_t)(cnt - 1) << 21);
+}
+struct Entry {
+  int e, row0, cnt;
+};
+__device__ __forceinline__ Entry read_entry(uint32_t v) {
+  return Entry{(int)(v & 1023u), (int)((v >> 10) & 2047u), (int)(v >> 21) + 1};
+}
+
+// The routing of every token, in LDS.
+struct Routing {
+  uint32_t entry[kMaxEntries];
+  int n_entries;
+  float row_w[kMaxRows];       // routing weight of a grouped row
+  uint8_t row_tok[kMaxRows];   // token of a grouped row
+};
+// What only the routing itself needs (it lies where the table will be).
+struct RouteScratch {
+  uint32_t mask[kMaxE][2];     // tokens that picked the expert
+  uint16_t off[kMaxE];         // first grouped row of the expert
+  uint16_t pick[kMaxRows];     // expert of slot t * top_k + j
+  float pick_w[kMaxRows];
+};
+
+// One wavefront's top-k of token t.  The picks are the k largest keys, equal
+// logits to the lower id: the k-th largest key is found bit by bit from the
+// top with ballot counts, stopping as soon as exactly k keys reach it.
+// Entry s of a lane is expert lane + 64 s.  Slots are in rank order where
+// the caller's workgroup writes the route's outputs, else in expert order.
+template <int EPL>
+__device__ void pick_token(const MoeLayerArgs& a, RouteScratch& L, int t, int lane, bool writer,
+                           const float (&val)[EPL]) {
+  uint32_t key[EPL];
+  uint32_t best = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[0][i] = load_frag(xrow, c * kStep + k_of<B>(g, i), a.H);
-        ag = step_mac<F, B, false, 1>(dg, x, lut, copy, ag);
-        au = step_mac<F, B, false, 1>(du, x, lut, copy, au);
-      }
+  for (int s = 0; s < EPL; ++s) {
+    // an entry that exists keeps a key above the absent ones' 0
+    key[s] = lane + kWave * s < a.E ? max(float_key(val[s]), 1u) : 0u;
+    best = max(best, key[s]);
+  }
+  best = wave_max_u32(best);
+  uint32_t th = 0;
+  for (int b = 31; b >= 0; --b) {
+    const uint32_t cand = th | (1u << b);
+    int cnt = 0;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        red[wave][0][(g * 4 + r) * 16 + col] = ag[r];
-        red[wave][1][(g * 4 + r) * 16 + col] = au[r];
-      }
-      __syncthreads();
-      if (threadIdx.x < 256) {
-        const int row = r0 + (threadIdx.x >> 4);
-        if (row < cnt) {
-          float gs = 0.0f, us = 0.0f;
+    for (int s = 0; s < EPL; ++s) cnt += __popcll(__builtin_amdgcn_ballot_w64(key[s] >= cand));
+    if (cnt >= a.top_k) {
+      th = cand;
+      if (cnt == a.top_k) break;
+    }
+  }
+  int need = a.top_k;  // of the keys equal to th, the lowest ids
 #pragma unroll
-          for (int k = 0; k < kGuWaves; ++k) {
-            gs += red[k][0][threadIdx.x];
-            us += red[k][1][threadIdx.x];
-          }
-          const float h = gs / (1.0f + expf(-gs)) * us * a.topk_w[a.sorted[off + row]];
-          const uint16_t hi = f32_to_bf16(h);
-          const size_t o = (size_t)(off + row) * a.I + n0 + (threadIdx.x & 15);
-          a.h_hi[o] = hi;
-          a.h_lo[o] = f32_to_bf16(h - bf16_to_f32(hi));
-        }
+  for (int s = 0; s < EPL; ++s) need -= __popcll(__builtin_amdgcn_ballot_w64(key[s] > th));
+  const float vbest = __uint_as_float((best & 0x80000000u) ? best ^ 0x80000000u : ~best);
+  bool sel[EPL];
+  float ex[EPL];
+  float part = 0.0f;
+#pragma unroll
+  for (int s = 0; s < EPL; ++s) {
+    const uint64_t eq = __builtin_amdgcn_ballot_w64(key[s] == th);
+    const int before = (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(eq >> 32),
+                                                      __builtin_amdgcn_mbcnt_lo((uint32_t)eq, 0u));
+    sel[s] = key[s] > th || (key[s] == th && before < need);
+    need = max(need - __popcll(eq), 0);
+    ex[s] = sel[s] ? expf(val[s] - vbest) : 0.0f;
+    part += ex[s];
+  }
+  const float sum = wave_sum_f32(part);
+  int slot[EPL];
+  int at = 0;
+  if (writer) {  // rank among the picks
+#pragma unroll
+    for (int s = 0; s < EPL; ++s) slot[s] = 0;
+#pragma unroll
+    for (int s2 = 0; s2 < EPL; ++s2) {
+      uint64_t m = __builtin_amdgcn_ballot_w64(sel[s2]);
+      while (m) {
+        const int src = __builtin_ctzll(m);
+        m &= m - 1;
+        const uint32_t kj = (uint32_t)__builtin_amdgcn_readlane((int)key[s2], src);
+        const int ej = src + kWave * s2;
+#pragma unroll
+        for (int s = 0; s < EPL; ++s)
+          slot[s] += (kj > key[s] || (kj == key[s] && ej < lane + kWave * s)) ? 1 : 0;
       }
-      __syncthreads();
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < EPL; ++s) {
+      const uint64_t m = __builtin_amdgcn_ballot_w64(sel[s]);
+      slot[s] = at + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
+                                                    __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+      at += __popcll(m);
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < EPL; ++s) {
+    if (sel[s]) {
+      const int e = lane + kWave * s, o = t * a.top_k + slot[s];
+      const float w = ex[s] / sum;
+      L.pick[o] = (uint16_t)e;
+      L.pick_w[o] = w;
+      atomicOr(&L.mask[e][t >> 5], 1u << (t & 31));
+      if (writer) {
+        a.topk_ids[o] = e;
+        a.topk_w[o] = w;
+      }
     }
   }
 }
 
-// down and the sum over each token's experts.  A workgroup owns 16 output
-// columns for every token and expert, so the sums stay on chip: the steps of
-// all routed experts are dealt to the wavefronts in equal contiguous ranges,
-// each wavefront adds into its own [token][column] sums in LDS, and the
-// wavefronts' sums are added in order.  No atomics, the same bits every run.
-template <W4 F, int B, typename S, int TMAX>
-__global__ __launch_bounds__(kDnWaves* kWave) void moe_down_kernel(MoeLayerArgs a) {
-  __shared__ __align__(16) char lut[F == W4::kMx4 ? 16 : kLutBytes];
-  __shared__ float sum[kDnWaves][TMAX * 16];
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  const int g = lane >> 4, col = lane & 15;
-  const int n0 = blockIdx.x * 16;
-  fill_lut<F>(lut);
-  for (int i = lane; i < TMAX * 16; i += kWave) sum[wave][i] = 0.0f;
-  __syncthreads();
-  const uint32_t copy = lut_copy<F>(lane);
-  const int steps = (a.I + kStep - 1) / kStep;
-  const int total = a.num_groups[0] * steps;
-  int s0 = (int)((int64_t)total * wave / kDnWaves);
-  const int s1 = (int)((int64_t)total * (wave + 1) / kDnWaves);
-  const size_t kb = a.I / 2, blocks = a.I / B;
-  while (s0 < s1) {
-    const int j = s0 / steps, c0 = s0 % steps;
-    const int c1 = min(steps, c0 + s1 - s0);
-    s0 += c1 - c0;
-    const int e = a.group_ids[j], cnt = a.group_sizes[j], off = a.offsets[e];
-    const size_t rn = (size_t)e * a.H + n0 + col;
-    const WeightRow<S> w = {a.dn_packed + rn * kb, static_cast<const S*>(a.dn_scales) + rn * blocks,
-                            nullptr};
-    for (int r0 = 0; r0 < cnt; r0 += 16) {
-      const size_t hr = (size_t)(off + min(r0 + col, cnt - 1)) * a.I;
-      f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int c = c0; c < c1; ++c) {
-        StepData<B, S> d;
-        load_step<B, false>(w, c, g, a.I, d);
-        bf16x8 x[2][4];
+template <int EPL>
+__device__ void pick_tokens(const MoeLayerArgs& a, RouteScratch& L, int wave, int lane, bool writer) {
+  float val[EPL], next[EPL];
+  const auto load = [&](int t, float (&v)[EPL]) {
+    const float* row = a.logits + (size_t)min(t, a.T - 1) * a.E;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[0][i] = load_frag(a.h_hi + hr, c * kStep + k_of<B>(g, i), a.I);
-          x[1][i] = load_frag(a.h_lo + hr, c * kStep + k_of<B>(g, i), a.I);
+    for (int s = 0; s < EPL; ++s) v[s] = row[min(lane + kWave * s, a.E - 1)];
+  };
+  load(wave, val);
+  for (int t = wave; t < a.T; t += kWaves) {
+    load(t + kWaves, next);
+    pick_token<EPL>(a, L, t, lane, writer, val);
+#pragma unroll
+    for (int s = 0; s < EPL; ++s) val[s] = next[s];
+  }
+}
+
+// Routes every token into LDS, and as the writing workgroup also into the
+// route's outputs and the lists the later launches read.
+__device__ void route_all(const MoeLayerArgs& a, Routing& L, RouteScratch& R, int wave, int lane,
+                          bool writer) {
+  for (int i = threadIdx.x; i < a.E; i += kThreads) {
+    R.mask[i][0] = 0u;
+    R.mask[i][1] = 0u;
+  }
+  lds_barrier();
+  if (a.E <= 64)
+    pick_tokens<1>(a, R, wave, lane, writer);
+  else if (a.E <= 128)
+    pick_tokens<2>(a, R, wave, lane, writer);
+  else if (a.E <= 256)
+    pick_tokens<4>(a, R, wave, lane, writer);
+  else
+    pick_tokens<16>(a, R, wave, lane, writer);
+  lds_barrier();
+  if (wave == 0) {  // experts in ascending order: first rows and entries
+    int rows = 0, entries = 0;
+    for (int e0 = 0; e0 < a.E; e0 += kWave) {
+      const int e = e0 + lane;
+      const int cnt = e < a.E ? __popc(R.mask[e][0]) + __popc(R.mask[e][1]) : 0;
+      const int tiles = (cnt + 15) >> 4;
+      const int cinc = wave_incl_scan(cnt), tinc = wave_incl_scan(tiles);
+      const int row = rows + cinc - cnt;
+      if (e < a.E) R.off[e] = (uint16_t)row;
+      for (int i = 0; i < tiles; ++i) {
+        const uint32_t v = make_entry(e, row + 16 * i, min(cnt - 16 * i, 16));
+        const int at = entries + tinc - tiles + i;
+        L.entry[at] = v;
+        if (writer) a.entries[1 + at] = v;
+      }
+      rows += __builtin_amdgcn_readlane(cinc, kWave - 1);
+      entries += __builtin_amdgcn_readlane(tinc, kWave - 1);
+    }
+    if (lane == 0) {
+      L.n_entries = entries;
+      if (writer) a.entries[0] = (uint32_t)entries;
+    }
+  }
+  lds_barrier();
+  for (int s = threadIdx.x; s < a.T * a.top_k; s += kThreads) {
+    const int t = s / a.top_k, e = R.pick[s];
+    const uint64_t m = (uint64_t)R.mask[e][0] | ((uint64_t)R.mask[e][1] << 32);
+    const int row = R.off[e] + __popcll(m & ((1ull << t) - 1ull));
+    L.row_tok[row] = (uint8_t)t;
+    L.row_w[row] = R.pick_w[s];
+    if (writer) a.slot_rows[s] = row;
+  }
+  lds_barrier();
+}
+
+// The work items of a projection: entry j's tiles, then entry j + 1's.
+struct ItemGrid {
+  int tiles;    // items per entry
+  int K;        // codes per weight row
+  int log_wk;   // wavefronts per team, as a power of two
+  int passes;   // over K, where an item's activations do not fit at once
+};
+
+// One set of the wavefronts' sums: 512 words per wavefront in the second halves
+// of the decode table's rows; two sets fill them.
+constexpr int kSumBytes = kWaves * 512 / 32 * 256;
+static_assert(2 * kSumBytes == kLutBytes, "two sets of sums beside the table");
+
+// Eight activations of a row at k, from the layer's input (bf16) or from h
+// (fp32): the largest magnitude's bits, and the values as scaled fp16.
+struct RawBf16 {
+  u32x4 v;
+  __device__ __forceinline__ void load(const uint16_t* x, uint32_t at) {
+    v = *reinterpret_cast<const u32x4*>(x + at);
+  }
+  __device__ __forceinline__ uint32_t max_bits() const {  // as fp32 bits
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      m = max(m, max((v[i] << 16) & 0x7fff0000u, v[i] & 0x7fff0000u));
+    return m;
+  }
+  __device__ __forceinline__ u32x4 half(float up) const {
+    u32x4 h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      h[i] = pack_f16x2(__uint_as_float(v[i] << 16) * up, __uint_as_float(v[i] & 0xffff0000u) * up);
+    return h;
+  }
+};
+struct RawF32 {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const float* x, uint32_t at) {
+    a = *reinterpret_cast<const f32x4*>(x + at);
+    b = *reinterpret_cast<const f32x4*>(x + at + 4);
+  }
+  __device__ __forceinline__ uint32_t max_bits() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      m = max(m, max(__float_as_uint(a[i]) & 0x7fffffffu, __float_as_uint(b[i]) & 0x7fffffffu));
+    return m;
+  }
+  __device__ __forceinline__ u32x4 half(float up) const {
+    return u32x4{pack_f16x2(a[0] * up, a[1] * up), pack_f16x2(a[2] * up, a[3] * up),
+                 pack_f16x2(b[0] * up, b[1] * up), pack_f16x2(b[2] * up, b[3] * up)};
+  }
+};
+
+// Workgroups per CU: two where a wavefront's activations leave its registers
+// room (their barriers then fall apart: one computes while the other waits).
+constexpr int groups_per_cu(int nst, int g) { return nst <= 2 && g == 1 ? 2 : 1; }
+constexpr int waves_per_simd(int nst, int g) { return groups_per_cu(nst, g) * kWaves / 4; }
+
+// The loop shared by the projections (see the head of the file); P says where
+// an item's weights and activations are and what becomes of its sums.  NST:
+// steps per wavefront and item whose activations fit the registers.  Longer
+// rows (G > 1) are walked in passes: G neighbouring items share each pass's
+// activations and keep their sums in registers from pass to pass.  Weight
+// addresses are a scalar base that the item and the step move and a lane offset
+// that never moves.
+template <W4 F, int B, typename S, int NST, int G, typename P>
+__device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int n_entries,
+                                             char* lut) {
+  constexpr int kBufs = NST == 3 ? 3 : 4, kAhead = kBufs - 1;
+  constexpr int kUnroll = G > 1 || NST >= kBufs ? 1 : kBufs / NST;  // items per turn of the loop
+  static_assert(NST * G * kUnroll % kBufs == 0, "a step's buffer must be known when compiling");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const int g = lane >> 4, col = lane & 15;
+  const int wk = 1 << ig.log_wk, teams = kWaves >> ig.log_wk;
+  const int team = wave >> ig.log_wk, kw = wave & (wk - 1);
+  const int K = ig.K, kb = K / 2, blocks = K / B;
+  const int steps = (K + kStep - 1) / kStep;
+  const uint32_t copy = lut_copy(lane);
+  // this team's groups of G items; every team makes as many rounds as the longest
+  const int groups = n_entries * (ig.tiles / G), n_teams = (int)gridDim.x * teams;
+  const int share = groups / n_teams, extra = groups - share * n_teams;
+  const int tid = (int)blockIdx.x * teams + team;
+  const int i0 = min(tid * share + min(tid, extra), groups - 1) * G;
+  const int n_mine = share + (tid < extra ? 1 : 0);
+  const int rounds = share + ((int)blockIdx.x * teams < extra ? 1 : 0);
+  if (rounds == 0) return;
+
+  // load side: the group, pass and item that the next loads belong to
+  int lj = i0 / ig.tiles, lt = i0 - lj * ig.tiles;
+  int cj = lj, ct = lt;   // and the group whose sums are being formed
+  int left = n_mine - 1;  // groups after it
+  int lp = 0, lg = 0;
+  const uint32_t coff = (uint32_t)(col * kb + g * 16), soff = (uint32_t)(col * blocks * sizeof(S));
+  const uint8_t* cbase;
+  const char* sbase;
+  const auto set_item = [&]() {
+    const uint32_t ev = (uint32_t)__builtin_amdgcn_readfirstlane((int)p.entry(lj));
+    const size_t row =
+        (size_t)read_entry(ev).e * p.expert_rows + (size_t)((lt + lg) * P::kTileRows);
+    cbase = p.codes + row * (size_t)kb;
+    sbase = reinterpret_cast<const char*>(p.scales) + row * (size_t)blocks * sizeof(S);
+  };
+  const auto next_item = [&]() {  // past the last group: the last one again
+    if constexpr (G > 1) {
+      if (++lg < G) return set_item();
+      lg = 0;
+      if (++lp < ig.passes) return set_item();
+      lp = 0;
+    }
+    if (left > 0) {
+      --left;
+      lt += G;
+      if (lt == ig.tiles) {
+        lt = 0;
+        ++lj;
+      }
+      set_item();
+    }
+  };
+  const auto load = [&](WeightStep<B, S> (&w)[2], int i) {
+    const int c = min((lp * NST + i) * wk + kw, steps - 1);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      load_weights<B, S>(cbase + (size_t)u * p.second * kb,
+                         sbase + (size_t)u * p.second * blocks * sizeof(S), c, coff, soff, g, kb,
+                         blocks, w[u]);
+  };
+  // The entry's activations at this wavefront's steps of a pass, each row
+  // scaled by its largest value there; `down` undoes it for the rows whose sums
+  // the lane holds (the row of lane l here is l % 16, of its sums
+  // 4 (l / 16) + r).
+  u32x4 x[NST][4];
+  f32x4 down;
+  const auto load_x = [&](int j, int pass) {
+    const Entry en = read_entry((uint32_t)__builtin_amdgcn_readfirstlane((int)p.entry(j)));
+    const uint32_t row =
+        (uint32_t)p.row(en.row0 + min(col, en.cnt - 1)) * (uint32_t)K + k_of<B>(g, 0);
+    // Register i of a step lies in a block that is in the row or past it as a
+    // whole (K is a multiple of the block); past it, the row's start is read
+    // and multiplied by zero.
+    const auto inside = [&](int n, int i) {
+      return ((pass * NST + n) * wk + kw) * kStep + (B == 64 ? (i >> 1) * 64 : i * B) < K;
+    };
+    const auto raw = [&](int n, int i) {
+      typename P::Raw v;
+      const int k = ((pass * NST + n) * wk + kw) * kStep + (k_of<B>(0, i) - k_of<B>(0, 0));
+      v.load(p.x + (inside(n, i) ? k : 0), row);
+      return v;
+    };
+    typename P::Raw keep[P::kKeepRaw ? NST : 1][4];
+    uint32_t top = 0;
+#pragma unroll
+    for (int n = 0; n < NST; ++n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) keep[P::kKeepRaw ? n : 0][i] = raw(n, i);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t m = keep[P::kKeepRaw ? n : 0][i].max_bits();
+        top = max(top, inside(n, i) ? m : 0u);
+      }
+    }
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16, kWave));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32, kWave));
+    const RowScale rs = {(int)(top >> 23)};
+    const float up = rs.up();
+#pragma unroll
+    for (int n = 0; n < NST; ++n) {
+      if constexpr (!P::kKeepRaw)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) keep[0][i] = raw(n, i);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[n][i] = keep[P::kKeepRaw ? n : 0][i].half(inside(n, i) ? up : 0.0f);
+      if constexpr (!P::kKeepRaw) __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) down[r] = __shfl(rs.down(), g * 4 + r, kWave);
+  };
+
+  set_item();
+  WeightStep<B, S> w[kBufs][2];
+#pragma unroll
+  for (int n = 0; n < kAhead; ++n) {
+    load(w[n], n % NST);
+    if (n % NST == NST - 1) next_item();
+  }
+  // an item's steps of a pass; `it` is its position within a turn of the loop
+  const auto item_steps = [&](int it, int pass, f32x4 (&acc)[2]) {
+    acc[0] = acc[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int n = 0; n < NST; ++n) {
+      const int q = it * NST + n;
+      load(w[(q + kAhead) % kBufs], (n + kAhead) % NST);
+      if ((n + kAhead) % NST == NST - 1) next_item();
+      __builtin_amdgcn_sched_barrier(0);  // the loads go first
+      // idle steps past the row's end have zero activations
+      const int late = scales_late<B>(min((pass * NST + n) * wk + kw, steps - 1), blocks);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        acc[h] = step_mac<F, B>(w[q % kBufs][h], late, x[n], lut, copy, acc[h]);
+        // where registers are short, one tile's decode at a time
+        if constexpr (G > 1 || F == W4::kMx4) __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[h][r] *= down[r];
+  };
+  // the wavefronts' sums of an item meet: [wave][tile][register][lane]
+  int turn = 0;
+  const auto meet = [&](const f32x4 (&acc)[2], int tile, bool mine) {
+    char* sums = lut + (turn & 1) * kSumBytes;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<float*>(
+            sums + lds_half(((wave * 2 + h) * 4 + r) * kWave) + lds_half(lane) - 128) = acc[h][r];
+    lds_barrier();
+    if (mine) p.finish(team, ig.log_wk, turn, cj, tile, sums);
+    ++turn;
+  };
+  if constexpr (G == 1) {
+    load_x(cj, 0);
+    for (;;) {
+#pragma unroll
+      for (int it = 0; it < kUnroll; ++it) {
+        f32x4 acc[2];
+        item_steps(it, 0, acc);
+        meet(acc, ct, turn < n_mine);
+        if (turn == rounds) return;
+        if (turn < n_mine && ++ct == ig.tiles) {
+          ct = 0;
+          load_x(++cj, 0);
         }
-        acc = step_mac<F, B, false, 2>(d, x, lut, copy, acc);
+      }
+    }
+  } else {
+    for (int round = 0; round < rounds; ++round) {
+      f32x4 total[G][2];
+#pragma unroll
+      for (int it = 0; it < G; ++it) total[it][0] = total[it][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int pass = 0; pass < ig.passes; ++pass) {
+        load_x(cj, pass);
+#pragma unroll
+        for (int it = 0; it < G; ++it) {
+          f32x4 acc[2];
+          item_steps(it, pass, acc);
+          total[it][0] += acc[0];
+          total[it][1] += acc[1];
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = r0 + g * 4 + r;
-        if (row < cnt) sum[wave][(a.sorted[off + row] / a.top_k) * 16 + col] += acc[r];
+      for (int it = 0; it < G; ++it) meet(total[it], ct + it, round < n_mine);
+      if (round + 1 < n_mine) {
+        ct += G;
+        if (ct == ig.tiles) {
+          ct = 0;
+          ++cj;
+        }
       }
     }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.T * 16; i += kDnWaves * kWave) {
-    const size_t o = (size_t)(i >> 4) * a.H + n0 + (i & 15);
-    float y = a.residual ? bf16_to_f32(a.residual[o]) : 0.0f;
-#pragma unroll
-    for (int k = 0; k < kDnWaves; ++k) y += sum[k][i];
-    a.out[o] = f32_to_bf16(y);
+}
+
+// Output o (0..255) of a tile: register o / 64 of lane o % 64.
+__device__ __forceinline__ int tile_row(int o) { return ((o & 63) >> 4) * 4 + (o >> 6); }
+__device__ __forceinline__ int tile_col(int o) { return o & 15; }
+
+// The sum of a team's wavefronts, in wavefront order.
+__device__ __forceinline__ float team_sum(const char* sums, int team, int log_wk, int tile, int o) {
+  const char* p = sums + lds_half((((team << log_wk) * 2 + tile) << 8) + o);
+  float v = 0.0f;
+  for (int k = 0; k < 1 << log_wk; k += 2) {
+    v += *reinterpret_cast<const float*>(p + k * (512 / 32 * 256));
+    v += *reinterpret_cast<const float*>(p + (k + 1) * (512 / 32 * 256));
   }
+  return v;
+}
+
+// gate_up: 16 gate rows and their 16 up rows; SwiGLU, scaled by the row's
+// routing weight (so the sums over a token's experts need no further factor)
+// and kept in fp32: one rounding to bf16 would cost as much accuracy as the
+// layer's output rounding.
+template <typename S>
+struct GateUp {
+  typedef RawBf16 Raw;
+  static constexpr bool kKeepRaw = true;
+  static constexpr int kTileRows = 16;
+  const MoeLayerArgs& a;
+  const Routing& L;
+  const uint8_t* codes;
+  const S* scales;
+  size_t expert_rows;
+  int second;  // rows from an item's first tile to its second
+  const uint16_t* x;
+  __device__ uint32_t entry(int j) const { return L.entry[j]; }
+  __device__ int row(int r) const { return L.row_tok[r]; }
+  __device__ void finish(int team, int log_wk, int round, int j, int tile,
+                         const char* sums) const {
+    const Entry en = read_entry(L.entry[j]);
+    const int n = 64 << log_wk;
+    // 256 outputs; the wavefronts of a wide team take turns
+    for (int o = ((int)threadIdx.x + round * 256) & (n - 1); o < 256; o += n) {
+      const int row = tile_row(o);
+      if (row >= en.cnt) continue;
+      const float gs = team_sum(sums, team, log_wk, 0, o), us = team_sum(sums, team, log_wk, 1, o);
+      a.h[(uint32_t)((en.row0 + row) * a.I + tile * 16 + tile_col(o))] =
+          gs / (1.0f + expf(-gs)) * us * L.row_w[en.row0 + row];
+    }
+  }
+};
+
+template <W4 F, int B, typename S, int NST, int G>
+__global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void moe_gate_up_kernel(MoeLayerArgs a, ItemGrid ig) {
+  __shared__ __align__(256) char lut[kLutBytes];
+  __shared__ Routing L;
+  static_assert(sizeof(RouteScratch) <= sizeof(lut), "the routing's scratch lies in the table");
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  route_all(a, L, *reinterpret_cast<RouteScratch*>(lut), wave, lane, blockIdx.x == 0);
+  fill_lut<F>(lut);
+  lds_barrier();
+  const GateUp<S> p = {a, L, a.gu_packed, static_cast<const S*>(a.gu_scales),
+                       2 * (size_t)a.I, a.I, a.x};
+  expert_tiles<F, B, S, NST, G>(p, ig, L.n_entries, lut);
+}
+
+// down: 32 weight rows, fp32 sums per grouped row.
+template <typename S>
+struct Down {
+  typedef RawF32 Raw;
+  static constexpr bool kKeepRaw = false;  // fp32 values of all steps do not fit; read twice
+  static constexpr int kTileRows = 32;
+  const MoeLayerArgs& a;
+  const uint32_t* entries;
+  const uint8_t* codes;
+  const S* scales;
+  size_t expert_rows;
+  int second;
+  const float* x;
+  __device__ uint32_t entry(int j) const { return entries[j]; }
+  __device__ int row(int r) const { return r; }
+  __device__ void finish(int team, int log_wk, int round, int j, int tile,
+                         const char* sums) const {
+    const Entry en = read_entry(entries[j]);
+    const int n = 64 << log_wk;
+    for (int i = ((int)threadIdx.x + round * 512) & (n - 1); i < 512; i += n) {
+      const int h = i >> 8, o = i & 255, row = tile_row(o);
+      if (row < en.cnt)
+        a.y[(size_t)(en.row0 + row) * a.H + tile * 32 + h * 16 + tile_col(o)] =
+            team_sum(sums, team, log_wk, h, o);
+    }
+  }
+};
+
+template <W4 F, int B, typename S, int NST, int G>
+__global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void moe_down_kernel(MoeLayerArgs a, ItemGrid ig,
+                                                            int max_entries) {
+  __shared__ __align__(256) char lut[kLutBytes];
+  __shared__ uint32_t entries[1 + kMaxEntries];
+  for (int i = threadIdx.x; i <= max_entries; i += kThreads) entries[i] = a.entries[i];
+  fill_lut<F>(lut);
+  lds_barrier();
+  const Down<S> p = {a, entries + 1, a.dn_packed, static_cast<const S*>(a.dn_scales),
+                     (size_t)a.H, 16, a.h};
+  expert_tiles<F, B, S, NST, G>(p, ig, (int)entries[0], lut);
+}
+
+// out[t] = residual[t] + the fp32 rows of the token's slots, in slot order.
+constexpr int kSumThreads = 256;
+
+__global__ __launch_bounds__(kSumThreads) void moe_sum_kernel(MoeLayerArgs a) {
+  const int q = blockIdx.x * kSumThreads + threadIdx.x;  // four columns each
+  if (q >= a.H / 4) return;
+  const int t = blockIdx.y;
+  const size_t o = (size_t)t * a.H + q * 4;
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (a.residual)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = bf16_to_f32(a.residual[o + i]);
+  for (int j = 0; j < a.top_k; ++j)
+    v += *reinterpret_cast<const f32x4*>(a.y + (size_t)a.slot_rows[t * a.top_k + j] * a.H + q * 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a.out[o + i] = f32_to_bf16(v[i]);
+}
+
+// Wavefronts per team, hence steps per wavefront: the widest team, with the
+// fewest activations to load and hold per wavefront, unless a narrower one
+// takes at least an eighth fewer steps in all when `entries` are routed (a team
+// wider than the row's steps has idle wavefronts).  A wavefront holds the
+// activations of at most four steps; longer rows take passes of four by the
+// whole workgroup.
+struct Launch {
+  unsigned grid;
+  int nst, group;
+  ItemGrid ig;
+};
+Launch plan_launch(int entries, int max_entries, int tiles, int K, int wide_group) {
+  const int steps = (K + kStep - 1) / kStep;
+  const int64_t cus = device_cu_count(), items = (int64_t)entries * tiles;
+  int best = 3, nst = (steps + 7) / 8, group = 1, passes = 1;
+  if (nst > 4) {
+    passes = (nst + 3) / 4;
+    nst = 4;
+    group = wide_group;
+  } else {
+    int64_t best_cost = INT64_MAX;
+    for (int l = 3; l >= 1; --l) {
+      const int n = (steps + (1 << l) - 1) >> l;
+      const int64_t teams = cus * groups_per_cu(n, 1) * (kWaves >> l);
+      const int64_t cost = (items + teams - 1) / teams * n * groups_per_cu(n, 1);
+      if (n <= 4 && cost < best_cost) {
+        best = l;
+        nst = n;
+        best_cost = cost * 7 / 8;
+      }
+    }
+  }
+  const int teams = kWaves >> best;
+  const int64_t need = ((int64_t)max_entries * (tiles / group) + teams - 1) / teams;
+  const int64_t room = cus * groups_per_cu(nst, group);
+  return Launch{(unsigned)(need < room ? need : room), nst, group, ItemGrid{tiles, K, best, passes}};
+}
+
+template <W4 F, int B, typename S, int NST, int G>
+void launch_gate_up(const MoeLayerArgs& a, const Launch& l, hipStream_t stream) {
+  hipLaunchKernelGGL((moe_gate_up_kernel<F, B, S, NST, G>), dim3(l.grid), dim3(kThreads), 0,
+                     stream, a, l.ig);
+}
+template <W4 F, int B, typename S, int NST, int G>
+void launch_down(const MoeLayerArgs& a, const Launch& l, int max_entries, hipStream_t stream) {
+  hipLaunchKernelGGL((moe_down_kernel<F, B, S, NST, G>), dim3(l.grid), dim3(kThreads), 0, stream,
+                     a, l.ig, max_entries);
 }
 
 template <W4 F, int B, typename S>
 void launch_layer(const MoeLayerArgs& a, hipStream_t stream) {
-  const int64_t groups = a.E < a.T * a.top_k ? a.E : a.T * a.top_k;
-  const int64_t items = groups * (a.I / 16);
-  const int64_t cap = 2 * (int64_t)device_cu_count();
-  hipLaunchKernelGGL((moe_gate_up_kernel<F, B, S>), dim3((unsigned)(items < cap ? items : cap)),
-                     dim3(kGuWaves * kWave), 0, stream, a);
-  if (a.T <= 16)
-    hipLaunchKernelGGL((moe_down_kernel<F, B, S, 16>), dim3(a.H / 16), dim3(kDnWaves * kWave), 0,
-                       stream, a);
+  const int rows = a.T * a.top_k;
+  const int experts = a.E < rows ? a.E : rows, max_entries = experts + rows / 16;
+  const Launch gu = plan_launch(experts, max_entries, a.I / 16, a.H, kGuGroup);
+  if (gu.group > 1)
+    launch_gate_up<F, B, S, 4, kGuGroup>(a, gu, stream);
+  else if (gu.nst == 1)
+    launch_gate_up<F, B, S, 1, 1>(a, gu, stream);
+  else if (gu.nst == 2)
+    launch_gate_up<F, B, S, 2, 1>(a, gu, stream);
+  else if (gu.nst == 3)
+    launch_gate_up<F, B, S, 3, 1>(a, gu, stream);
   else
-    hipLaunchKernelGGL((moe_down_kernel<F, B, S, kMoeLayerMaxTokens>), dim3(a.H / 16),
-                       dim3(kDnWaves * kWave), 0, stream, a);
+    launch_gate_up<F, B, S, 4, 1>(a, gu, stream);
+  const Launch dn = plan_launch(experts, max_entries, a.H / 32, a.I, kDnGroup);
+  if (dn.group > 1)
+    launch_down<F, B, S, 4, kDnGroup>(a, dn, max_entries, stream);
+  else if (dn.nst == 1)
+    launch_down<F, B, S, 1, 1>(a, dn, max_entries, stream);
+  else if (dn.nst == 2)
+    launch_down<F, B, S, 2, 1>(a, dn, max_entries, stream);
+  else if (dn.nst == 3)
+    launch_down<F, B, S, 3, 1>(a, dn, max_entries, stream);
+  else
+    launch_down<F, B, S, 4, 1>(a, dn, max_entries, stream);
+  hipLaunchKernelGGL(moe_sum_kernel, dim3((a.H / 4 + kSumThreads - 1) / kSumThreads, a.T),
+                     dim3(kSumThreads), 0, stream, a);
 }
 
 }  // namespace

@@ -21,15 +21,18 @@
 // no product of a code and a scale is ever rounded.
 //
 // Decode: one LDS read per byte (two codes) from a table of all 256 bytes,
-// replicated so that every lane has its own banks (64 copies of a 4-byte
-// entry, 32 of an 8-byte one: 64 KB).  An entry's address is byte << 8 | the
-// lane's copy, which one v_perm_b32 builds straight from the loaded dword.
-//  * int4: the entry is the pair q - 8 as bf16, exact;
-//  * NF4: a level is not a bf16 number, so the entry is two pairs, the
-//    level rounded to bf16 and the rest rounded to bf16 (together within
-//    2^-17 of the level), and the step issues two MFMAs;
-//  * MXFP4: E2M1 values are exact in bf16 and gfx950 converts them, two per
+// replicated so that the 32 lanes an LDS cycle serves have their own banks (32
+// copies of a 4-byte entry).  An entry's address is byte << 8 | the lane's
+// copy, which one v_perm_b32 builds straight from the loaded dword; the other
+// half of each 256-byte table row holds the workgroup's own data (lds_half).
+//  * int4: the entry is the pair q - 8 as bf16, exact, and meets the bf16
+//    activations as they are;
+//  * NF4: the entry is the pair of levels as fp16, each rounded once (2^-11
+//    of its value at most; bf16's 2^-8 would show beside the output's
+//    rounding, and a second bf16 term would double the reads and products);
+//  * MXFP4: E2M1 values are exact in fp16 and gfx950 converts them, two per
 //    instruction, with no table.
+// The fp16 formats need activations in fp16's range: see RowScale.
 #pragma once
 
 #include "gnf4_internal.h"
@@ -37,7 +40,8 @@
 namespace gnf4 {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -51,6 +55,9 @@ __device__ __forceinline__ int lane_id() {
   return (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
 }
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, (half2v{(_Float16)lo, (_Float16)hi}));
+}
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return (uint32_t)f32_to_bf16(lo) | ((uint32_t)f32_to_bf16(hi) << 16);
 }
@@ -65,13 +72,20 @@ __device__ __forceinline__ float scale_f32(float s) { return s; }
 __device__ __forceinline__ float scale_f32(uint16_t s) { return bf16_to_f32(s); }
 __device__ __forceinline__ float scale_f32(uint8_t s) { return e8m0_f32(s); }
 
+__device__ __forceinline__ uint32_t widen(float s) { return __float_as_uint(s); }
+__device__ __forceinline__ uint32_t widen(uint16_t s) { return s; }
+__device__ __forceinline__ uint32_t widen(uint8_t s) { return s; }
+
+// Byte address of the i-th 4-byte word kept in the table rows' second halves.
+__device__ __forceinline__ int lds_half(int i) { return (i >> 5) * 256 + 128 + (i & 31) * 4; }
+
 // The decode table, filled by the whole workgroup (a barrier must follow).
-// Thread t writes a quarter of entry t / 4.
+// Thread t writes half of entry t / 2.
 template <W4 F>
 __device__ __forceinline__ void fill_lut(char* lut) {
   if constexpr (F != W4::kMx4) {
-    for (int t = threadIdx.x; t < 1024; t += blockDim.x) {
-      const int b = t >> 2, q = t & 3;
+    for (int t = threadIdx.x; t < 512; t += blockDim.x) {
+      const int b = t >> 1, q = t & 1;
       const int c0 = b >> 4, c1 = b & 15;  // first element in the high nibble
       u32x4 v;
       if constexpr (F == W4::kInt4) {
@@ -84,10 +98,8 @@ __device__ __forceinline__ void fill_lut(char* lut) {
           l0 = c0 == i ? nf4_level(i) : l0;
           l1 = c1 == i ? nf4_level(i) : l1;
         }
-        const uint32_t hi = pack_bf16x2(l0, l1);
-        const uint32_t lo = pack_bf16x2(l0 - __uint_as_float(hi << 16),
-                                        l1 - __uint_as_float(hi & 0xffff0000u));
-        v = u32x4{hi, lo, hi, lo};
+        const uint32_t p = pack_f16x2(l0, l1);
+        v = u32x4{p, p, p, p};
       }
       u32x4* row = reinterpret_cast<u32x4*>(lut + b * 256 + q * 64);
 #pragma unroll
@@ -96,56 +108,29 @@ __device__ __forceinline__ void fill_lut(char* lut) {
   }
 }
 
+// Eight codes of one dword as an MFMA operand, in k order: bf16 for int4,
+// fp16 for the others.
 template <W4 F>
-struct Operand {
-  bf16x8 hi;
-};
-template <>
-struct Operand<W4::kNf4> {
-  bf16x8 hi, lo;
-};
-
-// Eight codes of one dword as MFMA operands, in k order.
-template <W4 F>
-__device__ __forceinline__ Operand<F> decode8(uint32_t w, const char* lut, uint32_t copy) {
-  Operand<F> o;
+__device__ __forceinline__ u32x4 decode8(uint32_t w, const char* lut, uint32_t copy) {
   if constexpr (F == W4::kMx4) {
-    const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0);
-    const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1);
-    const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2);
-    const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3);
-    const u32x4 v = {__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1),
-                     __builtin_bit_cast(uint32_t, p2), __builtin_bit_cast(uint32_t, p3)};
-    o.hi = __builtin_bit_cast(bf16x8, v);
+    const half2v p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
+    const half2v p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
+    const half2v p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2);
+    const half2v p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
+    return u32x4{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1),
+                 __builtin_bit_cast(uint32_t, p2), __builtin_bit_cast(uint32_t, p3)};
   } else {
     // address: the byte in bits 8..15, this lane's copy in bits 0..7
-    const uint32_t a0 = __builtin_amdgcn_perm(w, copy, 0x0c0c0400u);
-    const uint32_t a1 = __builtin_amdgcn_perm(w, copy, 0x0c0c0500u);
-    const uint32_t a2 = __builtin_amdgcn_perm(w, copy, 0x0c0c0600u);
-    const uint32_t a3 = __builtin_amdgcn_perm(w, copy, 0x0c0c0700u);
-    if constexpr (F == W4::kInt4) {
-      const u32x4 v = {*reinterpret_cast<const uint32_t*>(lut + a0),
-                       *reinterpret_cast<const uint32_t*>(lut + a1),
-                       *reinterpret_cast<const uint32_t*>(lut + a2),
-                       *reinterpret_cast<const uint32_t*>(lut + a3)};
-      o.hi = __builtin_bit_cast(bf16x8, v);
-    } else {
-      const u32x2 e0 = *reinterpret_cast<const u32x2*>(lut + a0);
-      const u32x2 e1 = *reinterpret_cast<const u32x2*>(lut + a1);
-      const u32x2 e2 = *reinterpret_cast<const u32x2*>(lut + a2);
-      const u32x2 e3 = *reinterpret_cast<const u32x2*>(lut + a3);
-      o.hi = __builtin_bit_cast(bf16x8, (u32x4{e0.x, e1.x, e2.x, e3.x}));
-      o.lo = __builtin_bit_cast(bf16x8, (u32x4{e0.y, e1.y, e2.y, e3.y}));
-    }
+    const auto at = [lut](uint32_t addr) { return *reinterpret_cast<const uint32_t*>(lut + addr); };
+    return u32x4{at(__builtin_amdgcn_perm(w, copy, 0x0c0c0400u)),
+                 at(__builtin_amdgcn_perm(w, copy, 0x0c0c0500u)),
+                 at(__builtin_amdgcn_perm(w, copy, 0x0c0c0600u)),
+                 at(__builtin_amdgcn_perm(w, copy, 0x0c0c0700u))};
   }
-  return o;
 }
 
 // This lane's copy of the table entries (the low address byte).
-template <W4 F>
-__device__ __forceinline__ uint32_t lut_copy(int lane) {
-  return F == W4::kInt4 ? (uint32_t)lane * 4u : (uint32_t)(lane & 31) * 8u;
-}
+__device__ __forceinline__ uint32_t lut_copy(int lane) { return (uint32_t)(lane & 31) * 4u; }
 
 // Offset within a step of the eight codes that register i (0..3) of lane
 // group g holds after arrange<B>.
@@ -174,8 +159,122 @@ __device__ __forceinline__ void arrange(u32x4& d) {
   }
 }
 
-__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+// a: 16 activation rows, b: 16 weight rows; lane l holds 8 k of row l % 16.
+template <W4 F>
+__device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (F == W4::kInt4)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a),
+                                                  __builtin_bit_cast(half8, b), c, 0, 0, 0);
+}
+
+// Activations as fp16: a row's values are multiplied by the power of two that
+// puts the largest of them in [2^14, 2^15) (bf16 values within 2^28 of it then
+// convert exactly, fp32 ones keep 11 bits) and the sums by its inverse.
+struct RowScale {
+  int exp;  // the largest value's exponent field, biased
+  // Powers of two within fp32's normal range: a row of zeros or of the
+  // smallest numbers stops at 2^126, one with an infinity scales it to itself.
+  __device__ __forceinline__ float up() const {
+    return __uint_as_float((uint32_t)(254 - down_field()) << 23);
+  }
+  __device__ __forceinline__ float down() const {
+    return __uint_as_float((uint32_t)down_field() << 23);
+  }
+  // 2^(exp - 127 - 14) as an exponent field
+  __device__ __forceinline__ int down_field() const { return min(max(exp - 14, 1), 253); }
+};
+
+// A row's scales of one step, as loaded: neighbours share a register.
+template <int N, typename S>
+struct ScaleWords {
+  static constexpr int kWords = (N * (int)sizeof(S) + 3) / 4;
+  uint32_t v[kWords];
+  // Block b's scale, where the words start `late` blocks before the step's
+  // first (see load_weights); what lies past the row's end is 0 or the last
+  // block's.
+  __device__ __forceinline__ float at(int b, int late) const {
+    if constexpr (sizeof(S) == 4) return __uint_as_float(late > 0 ? v[kWords - 1] : v[b]);
+    if constexpr (sizeof(S) == 2) {
+      const uint32_t w = v[0] >> (16 * late);
+      return __uint_as_float((b & 1) ? w & 0xffff0000u : w << 16);
+    }
+    return e8m0_f32((v[0] >> (8 * late) >> (8 * b)) & 255u);
+  }
+};
+// How many blocks before step c's first its scales are read from.
+template <int B>
+__device__ __forceinline__ int scales_late(int c, int blocks) {
+  return blocks >= kStep / B ? max((c + 1) * (kStep / B) - blocks, 0) : 0;
+}
+
+// What one step reads of a weight row.
+template <int B, typename S>
+struct WeightStep {
+  u32x4 codes;
+  ScaleWords<kStep / B, S> scale;
+};
+
+// Step c of the rows at codes + coff and scales + soff (bytes; coff includes
+// the lane group's 16 bytes).  A row has kb bytes and `blocks` scales; past
+// its end a lane reads the step's first bytes again (the activations there
+// are zero), and the step's scales, one load whatever their alignment, start
+// early enough to end with the row.
+template <int B, typename S>
+__device__ __forceinline__ void load_weights(const uint8_t* codes, const char* scales, int c,
+                                             uint32_t coff, uint32_t soff, int g, int kb,
+                                             int blocks, WeightStep<B, S>& w) {
+  constexpr int N = kStep / B;
+  const uint32_t co = c * (kStep / 2) + g * 16 < kb ? coff : coff - (uint32_t)(g * 16);
+  w.codes = __builtin_nontemporal_load(
+      reinterpret_cast<const u32x4*>(codes + c * (kStep / 2) + co));
+  if (blocks >= N) {
+    struct __attribute__((packed, aligned(sizeof(S)))) Words {
+      uint32_t v[N * sizeof(S) / 4 > 0 ? N * sizeof(S) / 4 : 1];
+    };
+    const int first = c * N - scales_late<B>(c, blocks);
+    if constexpr (N * sizeof(S) >= 4) {
+      const Words r = *reinterpret_cast<const Words*>(scales + first * (int)sizeof(S) + soff);
+#pragma unroll
+      for (int i = 0; i < ScaleWords<N, S>::kWords; ++i) w.scale.v[i] = r.v[i];
+    } else {
+      w.scale.v[0] = *reinterpret_cast<const uint16_t*>(scales + first * (int)sizeof(S) + soff);
+    }
+  } else {  // K = 64, half a step: the row's own scales only
+    if constexpr (B == 32 && sizeof(S) == 1)
+      w.scale.v[0] = *reinterpret_cast<const uint16_t*>(scales + soff);
+    else if constexpr (sizeof(S) == 2)
+      w.scale.v[0] = *reinterpret_cast<const uint16_t*>(scales + soff);
+    else
+#pragma unroll
+      for (int i = 0; i < ScaleWords<N, S>::kWords; ++i)
+        w.scale.v[i] = *reinterpret_cast<const uint32_t*>(scales + soff);
+  }
+}
+
+// acc += (activations of the step) . (weights of the step)^T.
+template <W4 F, int B, typename S>
+__device__ __forceinline__ f32x4 step_mac(const WeightStep<B, S>& w, int late,
+                                          const u32x4 (&x)[4], const char* lut, uint32_t copy,
+                                          f32x4 acc) {
+  u32x4 d = w.codes;
+  arrange<B>(d);
+  constexpr int kPer = B / 32;  // MFMAs of 32 codes per block
+#pragma unroll
+  for (int b = 0; b < kStep / B; ++b) {
+    f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = b * kPer + j;
+      p = mfma16<F>(x[i], decode8<F>(d[i], lut, copy), p);
+    }
+    const float s = w.scale.at(b, late);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[r] = fmaf(s, p[r], acc[r]);
+  }
+  return acc;
 }
 
 // One lane's weight row: codes, scales and (int4) zero points, all of the
@@ -211,17 +310,14 @@ __device__ __forceinline__ void load_step(const WeightRow<S>& w, int c, int g, i
 }
 
 // Eight activations of one row at k, or zeros past the row's end.
-__device__ __forceinline__ bf16x8 load_frag(const uint16_t* row, int k, int K) {
+__device__ __forceinline__ u32x4 load_frag(const uint16_t* row, int k, int K) {
   u32x4 v = {0u, 0u, 0u, 0u};
   if (k < K) v = *reinterpret_cast<const u32x4*>(row + k);
-  return __builtin_bit_cast(bf16x8, v);
+  return v;
 }
 
-// acc += (activations of the step) . (weights of the step)^T, XP operands per
-// activation (1, or 2 where the activation is the sum of two bf16 numbers;
-// the product of the two low parts is below fp32's last bit and left out).
-template <W4 F, int B, bool ZP, int XP, typename S>
-__device__ __forceinline__ f32x4 step_mac(StepData<B, S> d, const bf16x8 (&x)[XP][4],
+template <int B, bool ZP, typename S>
+__device__ __forceinline__ f32x4 step_mac_zp(StepData<B, S> d, const u32x4 (&x)[4],
                                           const char* lut, uint32_t copy, f32x4 acc) {
   arrange<B>(d.codes);
   constexpr int kPer = B / 32;  // MFMAs of 32 codes per block
@@ -231,13 +327,10 @@ __device__ __forceinline__ f32x4 step_mac(StepData<B, S> d, const bf16x8 (&x)[XP
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = b * kPer + j;
-      const Operand<F> o = decode8<F>(d.codes[i], lut, copy);
-      if constexpr (F == W4::kNf4) p = mfma16(x[0][i], o.lo, p);
-      if constexpr (XP == 2) p = mfma16(x[1][i], o.hi, p);
-      p = mfma16(x[0][i], o.hi, p);
+      p = mfma16<W4::kInt4>(x[i], decode8<W4::kInt4>(d.codes[i], lut, copy), p);
       if constexpr (ZP) {  // (q - 8) - (z - 8), both exact in bf16
         const uint32_t z = pack_bf16x2((float)(8 - (int)d.zero[b]), (float)(8 - (int)d.zero[b]));
-        p = mfma16(x[0][i], __builtin_bit_cast(bf16x8, (u32x4{z, z, z, z})), p);
+        p = mfma16<W4::kInt4>(x[i], u32x4{z, z, z, z}, p);
       }
     }
     const float s = scale_f32(d.scale[b]);

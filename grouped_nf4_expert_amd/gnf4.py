@@ -118,7 +118,7 @@ def library():
     lib.gnf4_int4_linear.restype = ctypes.c_int
     lib.gnf4_int4_linear.argtypes = [vp, i64, vp, vp, i32, vp, i32, i64, i64, vp, vp, vp]
     lib.gnf4_moe_layer_workspace_size.restype = sz
-    lib.gnf4_moe_layer_workspace_size.argtypes = [i64, i64, i32, i64]
+    lib.gnf4_moe_layer_workspace_size.argtypes = [i64, i64, i32, i64, i64]
     lib.gnf4_moe_layer.restype = ctypes.c_int
     lib.gnf4_moe_layer.argtypes = [vp, i64, i64, i32, vp, vp, vp, vp, vp, i32, i64, i64, vp, vp,
                                    vp, vp, vp, sz, vp]
@@ -351,7 +351,7 @@ class MoeLayerBuffers:
         self.out = torch.empty((T, H), dtype=torch.bfloat16, device=device)
         self.topk_ids = torch.empty((T, top_k), dtype=torch.int32, device=device)
         self.topk_w = torch.empty((T, top_k), dtype=torch.float32, device=device)
-        self.ws_bytes = library().gnf4_moe_layer_workspace_size(T, E, top_k, I)
+        self.ws_bytes = library().gnf4_moe_layer_workspace_size(T, E, top_k, H, I)
         self.workspace = torch.empty(max(self.ws_bytes, 1), dtype=torch.uint8, device=device)
 
 

@@ -274,8 +274,9 @@ gnf4_status gnf4_moe_ffn_one_token(const float* logits, int64_t E, int32_t top_k
  *             gnf4_route_sort writes them
  *   h[t, j] = w[t, j] * silu(x[t] . Wg[ids[t, j]]^T) * (x[t] . Wu[ids[t, j]]^T)
  *   out[t]  = residual[t] + sum_j h[t, j] . Wd[ids[t, j]]^T
- * with every sum in fp32 and one rounding to bf16 at the end (h travels
- * between the two projections as the sum of two bf16 numbers).
+ * with every sum in fp32 and one rounding to bf16 at the end.  Operands of
+ * the matrix cores are fp16: NF4 levels rounded once, activations (x, h) times
+ * a power of two per row.
  *
  * Landing page "grouped-nf4-gemm": "Owns" (the grouped packed GEMM over NF4
  * and native MXFP4, the router, swiglu and combine glue) and "Use this when"
@@ -304,11 +305,11 @@ gnf4_status gnf4_moe_ffn_one_token(const float* logits, int64_t E, int32_t top_k
  * Experts no token picked are not read.  Scales must be finite (an E8M0 0xFF
  * is NaN and gives NaN in the outputs it reaches).  Deterministic.
  * Limits: 0 <= T <= 64, 1 <= E <= 1024, 1 <= top_k <= min(E, 32), H and I
- * positive multiples of 64, I * H, E * 2I and E * H below 2^31.
+ * multiples of 64 from 64 to 8192.
  * Errors: GNF4_ERR_INVALID_ARG, GNF4_ERR_UNSUPPORTED (a size above the
  * limits), GNF4_ERR_NOT_DEVICE_PTR, GNF4_ERR_WORKSPACE, GNF4_ERR_HIP.
  */
-size_t gnf4_moe_layer_workspace_size(int64_t T, int64_t E, int32_t top_k, int64_t I);
+size_t gnf4_moe_layer_workspace_size(int64_t T, int64_t E, int32_t top_k, int64_t H, int64_t I);
 
 gnf4_status gnf4_moe_layer(const float* logits, int64_t T, int64_t E, int32_t top_k,
                            const uint16_t* x, const uint8_t* gate_up_packed,

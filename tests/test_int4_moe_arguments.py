@@ -78,14 +78,14 @@ def test_moe_layer_arguments(lib):
                dict(gs=ctypes.c_void_p(0x1002)), dict(o=ctypes.c_void_p(0x1001)),
                dict(r=ctypes.c_void_p(0x1001)), dict(ws=ctypes.c_void_p(0x1004))):
         assert call(**kw) == INVALID, kw
-    for kw in (dict(T=65), dict(E=1025), dict(E=64, k=33), dict(H=2 ** 20, I=2 ** 12)):
+    for kw in (dict(T=65), dict(E=1025), dict(E=64, k=33), dict(H=8256), dict(I=8256)):
         assert call(**kw) == UNSUPPORTED, kw
-    need = lib.gnf4_moe_layer_workspace_size(2, 8, 2, 64)
+    need = lib.gnf4_moe_layer_workspace_size(2, 8, 2, 128, 64)
     assert need > 0
     assert call(ws=NULL) == WORKSPACE and call(n=need - 1) == WORKSPACE
     assert call(n=need) == NOT_DEVICE
     assert call(T=0) == OK
-    assert lib.gnf4_moe_layer_workspace_size(65, 8, 2, 64) == 0
+    assert lib.gnf4_moe_layer_workspace_size(65, 8, 2, 128, 64) == 0
 
 
 def test_python_checks():
