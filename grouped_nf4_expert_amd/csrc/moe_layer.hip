@@ -1,8 +1,10 @@
-// A whole mixture-of-experts layer for a few tokens: three launches.
+// A whole mixture-of-experts layer for a few tokens: three launches
+// (four for more than eight tokens).
 //
 //  1. moe_gate_up_kernel: routing, gate_up and SwiGLU.  Every workgroup routes
-//     all tokens itself (a few thousand logits; a launch of its own would cost
-//     more than the work) and then takes its share of the work items;
+//     all tokens itself and then takes its share of the work items.  Up to one
+//     token per wavefront it also picks each token's experts (a launch of its
+//     own would cost more than the work); for more, moe_pick_kernel comes first;
 //  2. moe_down_kernel: the down projection, one fp32 row per routed slot;
 //  3. moe_sum_kernel: each token's sum over its slots, and the residual.
 //
@@ -30,12 +32,13 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * kWave;
-// items of a group that shares the activations of a pass: gate_up's and down's
-// entries have multiples of 4 and of 2
-constexpr int kGuGroup = 2, kDnGroup = 2;
+constexpr int kGroup = 2;  // items of a group that shares the activations of a pass
 constexpr int kMaxE = 1024;
 constexpr int kMaxRows = kMoeLayerMaxTokens * 32;  // top_k <= 32
 constexpr int kMaxEntries = kMoeLayerMaxEntries;
+
+// A value that is the same in every lane, in a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -52,12 +55,12 @@ __device__ __forceinline__ Entry read_entry(uint32_t v) {
   return Entry{(int)(v & 1023u), (int)((v >> 10) & 2047u), (int)(v >> 21) + 1};
 }
 
-// The routing of every token, in LDS.
+// The routing of every token, in LDS behind the decode table: room for
+// max_entries entries and the call's rows.
 struct Routing {
-  uint32_t entry[kMaxEntries];
-  int n_entries;
-  float row_w[kMaxRows];       // routing weight of a grouped row
-  uint8_t row_tok[kMaxRows];   // token of a grouped row
+  uint32_t* entry;
+  float* row_w;       // routing weight of a grouped row
+  uint8_t* row_tok;   // token of a grouped row
 };
 // What only the routing itself needs (it lies where the table will be).
 struct RouteScratch {
@@ -65,22 +68,23 @@ struct RouteScratch {
   uint16_t off[kMaxE];         // first grouped row of the expert
   uint16_t pick[kMaxRows];     // expert of slot t * top_k + j
   float pick_w[kMaxRows];
+  int n_entries;
 };
 
 // One wavefront's top-k of token t.  The picks are the k largest keys, equal
 // logits to the lower id: the k-th largest key is found bit by bit from the
 // top with ballot counts, stopping as soon as exactly k keys reach it.
-// Entry s of a lane is expert lane + 64 s.  Slots are in rank order where
-// the caller's workgroup writes the route's outputs, else in expert order.
-template <int EPL>
-__device__ void pick_token(const MoeLayerArgs& a, RouteScratch& L, int t, int lane, bool writer,
-                           const float (&val)[EPL]) {
+// Entry s of a lane is expert lane + 64 s.  pick(slot, expert, weight) takes
+// each pick, in rank order if `ranked`, else in expert order.
+template <int EPL, typename Pick>
+__device__ __forceinline__ void top_k_token(const float (&val)[EPL], int E, int top_k, int lane,
+                                            bool ranked, const Pick& pick) {
   uint32_t key[EPL];
   uint32_t best = 0;
 #pragma unroll
   for (int s = 0; s < EPL; ++s) {
     // an entry that exists keeps a key above the absent ones' 0
-    key[s] = lane + kWave * s < a.E ? max(float_key(val[s]), 1u) : 0u;
+    key[s] = lane + kWave * s < E ? max(float_key(val[s]), 1u) : 0u;
     best = max(best, key[s]);
   }
   best = wave_max_u32(best);
@@ -90,32 +94,33 @@ __device__ void pick_token(const MoeLayerArgs& a, RouteScratch& L, int t, int la
     int cnt = 0;
 #pragma unroll
     for (int s = 0; s < EPL; ++s) cnt += __popcll(__builtin_amdgcn_ballot_w64(key[s] >= cand));
-    if (cnt >= a.top_k) {
+    if (cnt >= top_k) {
       th = cand;
-      if (cnt == a.top_k) break;
+      if (cnt == top_k) break;
     }
   }
-  int need = a.top_k;  // of the keys equal to th, the lowest ids
+  int need = top_k;  // of the keys equal to th, the lowest ids
 #pragma unroll
   for (int s = 0; s < EPL; ++s) need -= __popcll(__builtin_amdgcn_ballot_w64(key[s] > th));
   const float vbest = __uint_as_float((best & 0x80000000u) ? best ^ 0x80000000u : ~best);
+  const auto below = [](uint64_t m) {  // of m's lanes, those below this one
+    return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
+                                          __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+  };
   bool sel[EPL];
   float ex[EPL];
   float part = 0.0f;
 #pragma unroll
   for (int s = 0; s < EPL; ++s) {
     const uint64_t eq = __builtin_amdgcn_ballot_w64(key[s] == th);
-    const int before = (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(eq >> 32),
-                                                      __builtin_amdgcn_mbcnt_lo((uint32_t)eq, 0u));
-    sel[s] = key[s] > th || (key[s] == th && before < need);
+    sel[s] = key[s] > th || (key[s] == th && below(eq) < need);
     need = max(need - __popcll(eq), 0);
     ex[s] = sel[s] ? expf(val[s] - vbest) : 0.0f;
     part += ex[s];
   }
   const float sum = wave_sum_f32(part);
   int slot[EPL];
-  int at = 0;
-  if (writer) {  // rank among the picks
+  if (ranked) {
 #pragma unroll
     for (int s = 0; s < EPL; ++s) slot[s] = 0;
 #pragma unroll
@@ -132,64 +137,93 @@ __device__ void pick_token(const MoeLayerArgs& a, RouteScratch& L, int t, int la
       }
     }
   } else {
+    int at = 0;
 #pragma unroll
     for (int s = 0; s < EPL; ++s) {
       const uint64_t m = __builtin_amdgcn_ballot_w64(sel[s]);
-      slot[s] = at + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
-                                                    __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+      slot[s] = at + below(m);
       at += __popcll(m);
     }
   }
 #pragma unroll
-  for (int s = 0; s < EPL; ++s) {
-    if (sel[s]) {
-      const int e = lane + kWave * s, o = t * a.top_k + slot[s];
-      const float w = ex[s] / sum;
-      L.pick[o] = (uint16_t)e;
-      L.pick_w[o] = w;
-      atomicOr(&L.mask[e][t >> 5], 1u << (t & 31));
-      if (writer) {
-        a.topk_ids[o] = e;
-        a.topk_w[o] = w;
-      }
-    }
-  }
+  for (int s = 0; s < EPL; ++s)
+    if (sel[s]) pick(slot[s], lane + kWave * s, ex[s] / sum);
 }
 
 template <int EPL>
-__device__ void pick_tokens(const MoeLayerArgs& a, RouteScratch& L, int wave, int lane, bool writer) {
-  float val[EPL], next[EPL];
-  const auto load = [&](int t, float (&v)[EPL]) {
-    const float* row = a.logits + (size_t)min(t, a.T - 1) * a.E;
+__device__ __forceinline__ void load_logits(const MoeLayerArgs& a, int t, int lane,
+                                            float (&val)[EPL]) {
+  const float* row = a.logits + (size_t)t * a.E;
 #pragma unroll
-    for (int s = 0; s < EPL; ++s) v[s] = row[min(lane + kWave * s, a.E - 1)];
-  };
-  load(wave, val);
-  for (int t = wave; t < a.T; t += kWaves) {
-    load(t + kWaves, next);
-    pick_token<EPL>(a, L, t, lane, writer, val);
-#pragma unroll
-    for (int s = 0; s < EPL; ++s) val[s] = next[s];
-  }
+  for (int s = 0; s < EPL; ++s) val[s] = row[min(lane + kWave * s, a.E - 1)];
+}
+
+// The top-k of a batch too large for moe_gate_up_kernel to repeat in every
+// workgroup (more than a token per wavefront): one wavefront per token.
+template <int EPL>
+__global__ __launch_bounds__(kWave) void moe_pick_kernel(MoeLayerArgs a) {
+  const int t = blockIdx.x, lane = threadIdx.x;
+  float val[EPL];
+  load_logits<EPL>(a, t, lane, val);
+  top_k_token<EPL>(val, a.E, a.top_k, lane, true, [&](int slot, int e, float w) {
+    a.topk_ids[t * a.top_k + slot] = e;
+    a.topk_w[t * a.top_k + slot] = w;
+  });
+}
+
+__device__ __forceinline__ void set_pick(RouteScratch& R, int top_k, int t, int slot, int e,
+                                         float w) {
+  R.pick[t * top_k + slot] = (uint16_t)e;
+  R.pick_w[t * top_k + slot] = w;
+  atomicOr(&R.mask[e][t >> 5], 1u << (t & 31));
+}
+
+template <int EPL>
+__device__ void pick_own(const MoeLayerArgs& a, RouteScratch& R, int wave, int lane, bool writer) {
+  float val[EPL];
+  load_logits<EPL>(a, min(wave, a.T - 1), lane, val);
+  for (int i = threadIdx.x; i < a.E; i += kThreads) R.mask[i][0] = R.mask[i][1] = 0u;
+  lds_barrier();
+  if (wave < a.T)
+    top_k_token<EPL>(val, a.E, a.top_k, lane, writer, [&](int slot, int e, float w) {
+      set_pick(R, a.top_k, wave, slot, e, w);
+      if (writer) {
+        a.topk_ids[wave * a.top_k + slot] = e;
+        a.topk_w[wave * a.top_k + slot] = w;
+      }
+    });
 }
 
 // Routes every token into LDS, and as the writing workgroup also into the
 // route's outputs and the lists the later launches read.
-__device__ void route_all(const MoeLayerArgs& a, Routing& L, RouteScratch& R, int wave, int lane,
-                          bool writer) {
-  for (int i = threadIdx.x; i < a.E; i += kThreads) {
-    R.mask[i][0] = 0u;
-    R.mask[i][1] = 0u;
+__device__ int route_all(const MoeLayerArgs& a, const Routing& L, RouteScratch& R, int wave,
+                         int lane, bool writer) {
+  if (a.T > kWaves) {  // moe_pick_kernel has picked
+    const int rows = a.T * a.top_k;
+    int e[kMaxRows / kThreads];
+    float w[kMaxRows / kThreads];
+#pragma unroll
+    for (int i = 0; i < kMaxRows / kThreads; ++i) {
+      const int s = min((int)threadIdx.x + i * kThreads, rows - 1);
+      e[i] = a.topk_ids[s];
+      w[i] = a.topk_w[s];
+    }
+    for (int i = threadIdx.x; i < a.E; i += kThreads) R.mask[i][0] = R.mask[i][1] = 0u;
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < kMaxRows / kThreads; ++i) {
+      const int s = (int)threadIdx.x + i * kThreads;
+      if (s < rows) set_pick(R, a.top_k, s / a.top_k, s % a.top_k, e[i], w[i]);
+    }
+  } else if (a.E <= 64) {
+    pick_own<1>(a, R, wave, lane, writer);
+  } else if (a.E <= 128) {
+    pick_own<2>(a, R, wave, lane, writer);
+  } else if (a.E <= 256) {
+    pick_own<4>(a, R, wave, lane, writer);
+  } else {
+    pick_own<16>(a, R, wave, lane, writer);
   }
-  lds_barrier();
-  if (a.E <= 64)
-    pick_tokens<1>(a, R, wave, lane, writer);
-  else if (a.E <= 128)
-    pick_tokens<2>(a, R, wave, lane, writer);
-  else if (a.E <= 256)
-    pick_tokens<4>(a, R, wave, lane, writer);
-  else
-    pick_tokens<16>(a, R, wave, lane, writer);
   lds_barrier();
   if (wave == 0) {  // experts in ascending order: first rows and entries
     int rows = 0, entries = 0;
@@ -210,11 +244,12 @@ __device__ void route_all(const MoeLayerArgs& a, Routing& L, RouteScratch& R, in
       entries += __builtin_amdgcn_readlane(tinc, kWave - 1);
     }
     if (lane == 0) {
-      L.n_entries = entries;
+      R.n_entries = entries;
       if (writer) a.entries[0] = (uint32_t)entries;
     }
   }
   lds_barrier();
+  const int n_entries = uniform(R.n_entries);
   for (int s = threadIdx.x; s < a.T * a.top_k; s += kThreads) {
     const int t = s / a.top_k, e = R.pick[s];
     const uint64_t m = (uint64_t)R.mask[e][0] | ((uint64_t)R.mask[e][1] << 32);
@@ -224,6 +259,7 @@ __device__ void route_all(const MoeLayerArgs& a, Routing& L, RouteScratch& R, in
     if (writer) a.slot_rows[s] = row;
   }
   lds_barrier();
+  return n_entries;
 }
 
 // The work items of a projection: entry j's tiles, then entry j + 1's.
@@ -280,6 +316,22 @@ struct RawF32 {
   }
 };
 
+// The scales of a turn in LDS: step s of row r (0..31) of a team, rows side by
+// side, each step's a word further on so that a fetch's stores (neighbouring
+// lanes hold neighbouring steps) meet different banks.
+template <typename Scale>
+__device__ __forceinline__ int scale_at(int s, int r) {
+  return s * (32 * (int)sizeof(Scale) + 4 * Scale::kWords) + r * (int)sizeof(Scale);
+}
+template <typename Scale>
+__device__ __forceinline__ int team_scales(int nst, int team, int wk) {
+  return team * scale_at<Scale>(nst * wk, 0);
+}
+template <typename Scale>
+__host__ __device__ constexpr int scale_bytes(int nst) {
+  return kWaves * nst * (32 * (int)sizeof(Scale) + 4 * Scale::kWords);
+}
+
 // Workgroups per CU: two where a wavefront's activations leave its registers
 // room (their barriers then fall apart: one computes while the other waits).
 constexpr int groups_per_cu(int nst, int g) { return nst <= 2 && g == 1 ? 2 : 1; }
@@ -294,11 +346,14 @@ constexpr int waves_per_simd(int nst, int g) { return groups_per_cu(nst, g) * kW
 // that never moves.
 template <W4 F, int B, typename S, int NST, int G, typename P>
 __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int n_entries,
-                                             char* lut) {
+                                             char* lut, char* slds) {
+  typedef ScaleWord<B, S> Scale;
   constexpr int kBufs = NST == 3 ? 3 : 4, kAhead = kBufs - 1;
-  constexpr int kUnroll = G > 1 || NST >= kBufs ? 1 : kBufs / NST;  // items per turn of the loop
-  static_assert(NST * G * kUnroll % kBufs == 0, "a step's buffer must be known when compiling");
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  constexpr int kUnroll = NST == 1 ? 4 : 2;  // items per turn of the loop
+  static_assert(G == 1 || G == kUnroll, "a turn is a group's items");
+  static_assert(NST * kUnroll % kBufs == 0 && kUnroll % 2 == 0,
+                "the buffers of a step and of an item must be known when compiling");
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int g = lane >> 4, col = lane & 15;
   const int wk = 1 << ig.log_wk, teams = kWaves >> ig.log_wk;
   const int team = wave >> ig.log_wk, kw = wave & (wk - 1);
@@ -307,7 +362,7 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
   const uint32_t copy = lut_copy(lane);
   // this team's groups of G items; every team makes as many rounds as the longest
   const int groups = n_entries * (ig.tiles / G), n_teams = (int)gridDim.x * teams;
-  const int share = groups / n_teams, extra = groups - share * n_teams;
+  const int share = uniform(groups / n_teams), extra = groups - share * n_teams;
   const int tid = (int)blockIdx.x * teams + team;
   const int i0 = min(tid * share + min(tid, extra), groups - 1) * G;
   const int n_mine = share + (tid < extra ? 1 : 0);
@@ -315,44 +370,81 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
   if (rounds == 0) return;
 
   // load side: the group, pass and item that the next loads belong to
-  int lj = i0 / ig.tiles, lt = i0 - lj * ig.tiles;
+  int lj = uniform(i0 / ig.tiles), lt = i0 - lj * ig.tiles;
   int cj = lj, ct = lt;   // and the group whose sums are being formed
   int left = n_mine - 1;  // groups after it
   int lp = 0, lg = 0;
-  const uint32_t coff = (uint32_t)(col * kb + g * 16), soff = (uint32_t)(col * blocks * sizeof(S));
+  const uint32_t coff = (uint32_t)(col * kb + g * 16);
   const uint8_t* cbase;
-  const char* sbase;
-  const auto set_item = [&]() {
-    const uint32_t ev = (uint32_t)__builtin_amdgcn_readfirstlane((int)p.entry(lj));
-    const size_t row =
-        (size_t)read_entry(ev).e * p.expert_rows + (size_t)((lt + lg) * P::kTileRows);
-    cbase = p.codes + row * (size_t)kb;
-    sbase = reinterpret_cast<const char*>(p.scales) + row * (size_t)blocks * sizeof(S);
+  const auto weight_row = [&](int j, int tile) {  // of the stack
+    const uint32_t ev = (uint32_t)uniform((int)p.entry(j));
+    return (size_t)read_entry(ev).e * p.expert_rows + (size_t)(tile * P::kTileRows);
   };
-  const auto next_item = [&]() {  // past the last group: the last one again
+  const auto set_item = [&]() { cbase = p.codes + weight_row(lj, lt + lg) * (size_t)kb; };
+  // one item (of a pass) on; past the last group, the last one again
+  const auto step_on = [&](int& j, int& t, int& pass, int& item, int& rest) {
     if constexpr (G > 1) {
-      if (++lg < G) return set_item();
-      lg = 0;
-      if (++lp < ig.passes) return set_item();
-      lp = 0;
+      if (++item < G) return;
+      item = 0;
+      if (++pass < ig.passes) return;
+      pass = 0;
     }
-    if (left > 0) {
-      --left;
-      lt += G;
-      if (lt == ig.tiles) {
-        lt = 0;
-        ++lj;
+    if (rest > 0) {
+      --rest;
+      t += G;
+      if (t == ig.tiles) {
+        t = 0;
+        ++j;
       }
+    }
+  };
+  const auto load = [&](u32x4 (&w)[2], int i) {
+    const int c = min((lp * wk + kw) * NST + i, steps - 1);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      w[u] = load_codes(cbase + (size_t)u * p.second * kb, c, coff, g, kb);
+    if (i == NST - 1) {
+      step_on(lj, lt, lp, lg, left);
       set_item();
     }
   };
-  const auto load = [&](WeightStep<B, S> (&w)[2], int i) {
-    const int c = min((lp * NST + i) * wk + kw, steps - 1);
+  // Scales go through LDS: read by each lane from its own row they would cost
+  // as many cache lines as the codes.  The team's threads fetch the item's
+  // 2 x 16 rows of wk * NST steps in row order, two items ahead.
+  constexpr int kSteps = 32 * NST, kFetch = (kSteps + 63) / 64;  // words per wavefront, per thread
+  int fj = lj, ft = lt, fp = 0, fg = 0, fleft = left;
+  uint32_t foff[kFetch];
+  int fstep[kFetch], fat[kFetch];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-      load_weights<B, S>(cbase + (size_t)u * p.second * kb,
-                         sbase + (size_t)u * p.second * blocks * sizeof(S), c, coff, soff, g, kb,
-                         blocks, w[u]);
+  for (int i = 0; i < kFetch; ++i) {  // row, then step; threads left over repeat the last
+    const int id = min(kw * kWave + lane + i * (wk * kWave), (32 * NST << ig.log_wk) - 1);
+    const int row = id / NST >> ig.log_wk;
+    fstep[i] = id - ((row * NST) << ig.log_wk);
+    foff[i] = (uint32_t)(((row & 15) + (row & 16 ? p.second : 0)) * blocks * (int)sizeof(S));
+    if constexpr (G == 1) foff[i] += scales_first<B>(min(fstep[i], steps - 1), blocks) * sizeof(S);
+    fat[i] = team_scales<Scale>(NST, team, wk) + scale_at<Scale>(fstep[i], row);
+  }
+  Scale fetched[2][kFetch];
+  int fsteps[2] = {0, 0};  // the first step of a fetch
+  const auto fetch = [&](int buf) {
+    const char* sb = reinterpret_cast<const char*>(p.scales) +
+                     weight_row(fj, ft + fg) * (size_t)blocks * sizeof(S);
+    if constexpr (G > 1) fsteps[buf] = fp * wk * NST;
+#pragma unroll
+    for (int i = 0; i < kFetch; ++i) {
+      uint32_t at = foff[i];
+      if constexpr (G > 1)
+        at += scales_first<B>(min(fsteps[buf] + fstep[i], steps - 1), blocks) * sizeof(S);
+      load_scales<B, S>(sb, at, NST == 1 && blocks < kStep / B, fetched[buf][i]);
+    }
+    step_on(fj, ft, fp, fg, fleft);
+  };
+  const auto put = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < kFetch; ++i) {
+      align_scales<B, S>(fetched[buf][i], min(fsteps[buf] + fstep[i], steps - 1), blocks);
+      *reinterpret_cast<Scale*>(slds + buf * scale_bytes<Scale>(NST) + fat[i]) = fetched[buf][i];
+    }
   };
   // The entry's activations at this wavefront's steps of a pass, each row
   // scaled by its largest value there; `down` undoes it for the rows whose sums
@@ -361,18 +453,18 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
   u32x4 x[NST][4];
   f32x4 down;
   const auto load_x = [&](int j, int pass) {
-    const Entry en = read_entry((uint32_t)__builtin_amdgcn_readfirstlane((int)p.entry(j)));
+    const Entry en = read_entry((uint32_t)uniform((int)p.entry(j)));
     const uint32_t row =
         (uint32_t)p.row(en.row0 + min(col, en.cnt - 1)) * (uint32_t)K + k_of<B>(g, 0);
     // Register i of a step lies in a block that is in the row or past it as a
     // whole (K is a multiple of the block); past it, the row's start is read
     // and multiplied by zero.
     const auto inside = [&](int n, int i) {
-      return ((pass * NST + n) * wk + kw) * kStep + (B == 64 ? (i >> 1) * 64 : i * B) < K;
+      return ((pass * wk + kw) * NST + n) * kStep + (B == 64 ? (i >> 1) * 64 : i * B) < K;
     };
     const auto raw = [&](int n, int i) {
       typename P::Raw v;
-      const int k = ((pass * NST + n) * wk + kw) * kStep + (k_of<B>(0, i) - k_of<B>(0, 0));
+      const int k = ((pass * wk + kw) * NST + n) * kStep + (k_of<B>(0, i) - k_of<B>(0, 0));
       v.load(p.x + (inside(n, i) ? k : 0), row);
       return v;
     };
@@ -406,31 +498,36 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
     for (int r = 0; r < 4; ++r) down[r] = __shfl(rs.down(), g * 4 + r, kWave);
   };
 
+  fetch(0);
   set_item();
-  WeightStep<B, S> w[kBufs][2];
+  u32x4 w[kBufs][2];
 #pragma unroll
-  for (int n = 0; n < kAhead; ++n) {
-    load(w[n], n % NST);
-    if (n % NST == NST - 1) next_item();
-  }
+  for (int n = 0; n < kAhead; ++n) load(w[n], n % NST);
+  fetch(1);
+  put(0);
+  lds_barrier();
   // an item's steps of a pass; `it` is its position within a turn of the loop
-  const auto item_steps = [&](int it, int pass, f32x4 (&acc)[2]) {
+  const auto item_steps = [&](int it, f32x4 (&acc)[2]) {
     acc[0] = acc[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    fetch(it & 1);
+    const char* mine = slds + (it & 1) * scale_bytes<Scale>(NST) +
+                       team_scales<Scale>(NST, team, wk) + scale_at<Scale>(kw * NST, col);
 #pragma unroll
     for (int n = 0; n < NST; ++n) {
       const int q = it * NST + n;
       load(w[(q + kAhead) % kBufs], (n + kAhead) % NST);
-      if ((n + kAhead) % NST == NST - 1) next_item();
       __builtin_amdgcn_sched_barrier(0);  // the loads go first
       // idle steps past the row's end have zero activations
-      const int late = scales_late<B>(min((pass * NST + n) * wk + kw, steps - 1), blocks);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        acc[h] = step_mac<F, B>(w[q % kBufs][h], late, x[n], lut, copy, acc[h]);
+        const Scale sc = *reinterpret_cast<const Scale*>(mine + scale_at<Scale>(n, h * 16));
+        acc[h] = step_mac<F, B, S>(w[q % kBufs][h], sc, x[n], lut, copy, acc[h]);
         // where registers are short, one tile's decode at a time
-        if constexpr (G > 1 || F == W4::kMx4) __builtin_amdgcn_sched_barrier(0);
+        if constexpr (G > 1 || F == W4::kMx4 || groups_per_cu(NST, G) > 1)
+          __builtin_amdgcn_sched_barrier(0);
       }
     }
+    put((it + 1) & 1);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -456,7 +553,7 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
 #pragma unroll
       for (int it = 0; it < kUnroll; ++it) {
         f32x4 acc[2];
-        item_steps(it, 0, acc);
+        item_steps(it, acc);
         meet(acc, ct, turn < n_mine);
         if (turn == rounds) return;
         if (turn < n_mine && ++ct == ig.tiles) {
@@ -475,10 +572,10 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
 #pragma unroll
         for (int it = 0; it < G; ++it) {
           f32x4 acc[2];
-          item_steps(it, pass, acc);
+          item_steps(it, acc);
           total[it][0] += acc[0];
           total[it][1] += acc[1];
-          __builtin_amdgcn_sched_barrier(0);
+          lds_barrier();  // the next scales are in place, the last ones free
         }
       }
 #pragma unroll
@@ -543,17 +640,23 @@ struct GateUp {
 };
 
 template <W4 F, int B, typename S, int NST, int G>
-__global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void moe_gate_up_kernel(MoeLayerArgs a, ItemGrid ig) {
-  __shared__ __align__(256) char lut[kLutBytes];
-  __shared__ Routing L;
-  static_assert(sizeof(RouteScratch) <= sizeof(lut), "the routing's scratch lies in the table");
+__global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void moe_gate_up_kernel(MoeLayerArgs a, ItemGrid ig,
+                                                               int max_entries) {
+  extern __shared__ __align__(256) char lut[];
+  static_assert(sizeof(RouteScratch) <= kLutBytes, "the routing's scratch lies in the table");
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  route_all(a, L, *reinterpret_cast<RouteScratch*>(lut), wave, lane, blockIdx.x == 0);
+  char* slds = lut + kLutBytes;
+  Routing L;
+  L.entry = reinterpret_cast<uint32_t*>(slds + 2 * scale_bytes<ScaleWord<B, S>>(NST));
+  L.row_w = reinterpret_cast<float*>(L.entry + max_entries);
+  L.row_tok = reinterpret_cast<uint8_t*>(L.row_w + a.T * a.top_k);
+  const int n_entries =
+      route_all(a, L, *reinterpret_cast<RouteScratch*>(lut), wave, lane, blockIdx.x == 0);
   fill_lut<F>(lut);
   lds_barrier();
   const GateUp<S> p = {a, L, a.gu_packed, static_cast<const S*>(a.gu_scales),
                        2 * (size_t)a.I, a.I, a.x};
-  expert_tiles<F, B, S, NST, G>(p, ig, L.n_entries, lut);
+  expert_tiles<F, B, S, NST, G>(p, ig, n_entries, lut, slds);
 }
 
 // down: 32 weight rows, fp32 sums per grouped row.
@@ -587,14 +690,16 @@ struct Down {
 template <W4 F, int B, typename S, int NST, int G>
 __global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void moe_down_kernel(MoeLayerArgs a, ItemGrid ig,
                                                             int max_entries) {
-  __shared__ __align__(256) char lut[kLutBytes];
-  __shared__ uint32_t entries[1 + kMaxEntries];
+  extern __shared__ __align__(256) char lut[];
+  char* slds = lut + kLutBytes;
+  uint32_t* entries =
+      reinterpret_cast<uint32_t*>(slds + 2 * scale_bytes<ScaleWord<B, S>>(NST));
   for (int i = threadIdx.x; i <= max_entries; i += kThreads) entries[i] = a.entries[i];
   fill_lut<F>(lut);
   lds_barrier();
   const Down<S> p = {a, entries + 1, a.dn_packed, static_cast<const S*>(a.dn_scales),
                      (size_t)a.H, 16, a.h};
-  expert_tiles<F, B, S, NST, G>(p, ig, (int)entries[0], lut);
+  expert_tiles<F, B, S, NST, G>(p, ig, uniform((int)entries[0]), lut, slds);
 }
 
 // out[t] = residual[t] + the fp32 rows of the token's slots, in slot order.
@@ -626,14 +731,14 @@ struct Launch {
   int nst, group;
   ItemGrid ig;
 };
-Launch plan_launch(int entries, int max_entries, int tiles, int K, int wide_group) {
+Launch plan_launch(int entries, int max_entries, int tiles, int K) {
   const int steps = (K + kStep - 1) / kStep;
   const int64_t cus = device_cu_count(), items = (int64_t)entries * tiles;
   int best = 3, nst = (steps + 7) / 8, group = 1, passes = 1;
   if (nst > 4) {
     passes = (nst + 3) / 4;
     nst = 4;
-    group = wide_group;
+    group = kGroup;
   } else {
     int64_t best_cost = INT64_MAX;
     for (int l = 3; l >= 1; --l) {
@@ -654,34 +759,44 @@ Launch plan_launch(int entries, int max_entries, int tiles, int K, int wide_grou
 }
 
 template <W4 F, int B, typename S, int NST, int G>
-void launch_gate_up(const MoeLayerArgs& a, const Launch& l, hipStream_t stream) {
-  hipLaunchKernelGGL((moe_gate_up_kernel<F, B, S, NST, G>), dim3(l.grid), dim3(kThreads), 0,
-                     stream, a, l.ig);
+void launch_gate_up(const MoeLayerArgs& a, const Launch& l, int max_entries, hipStream_t stream) {
+  const int lds = kLutBytes + 2 * scale_bytes<ScaleWord<B, S>>(NST) + 4 * max_entries +
+                  5 * a.T * a.top_k;
+  hipLaunchKernelGGL((moe_gate_up_kernel<F, B, S, NST, G>), dim3(l.grid), dim3(kThreads), lds,
+                     stream, a, l.ig, max_entries);
 }
 template <W4 F, int B, typename S, int NST, int G>
 void launch_down(const MoeLayerArgs& a, const Launch& l, int max_entries, hipStream_t stream) {
-  hipLaunchKernelGGL((moe_down_kernel<F, B, S, NST, G>), dim3(l.grid), dim3(kThreads), 0, stream,
-                     a, l.ig, max_entries);
+  const int lds = kLutBytes + 2 * scale_bytes<ScaleWord<B, S>>(NST) + 4 * (1 + max_entries);
+  hipLaunchKernelGGL((moe_down_kernel<F, B, S, NST, G>), dim3(l.grid), dim3(kThreads), lds,
+                     stream, a, l.ig, max_entries);
 }
 
 template <W4 F, int B, typename S>
 void launch_layer(const MoeLayerArgs& a, hipStream_t stream) {
+  if (a.T > kWaves) {
+    const auto pick = a.E <= 64    ? moe_pick_kernel<1>
+                      : a.E <= 128 ? moe_pick_kernel<2>
+                      : a.E <= 256 ? moe_pick_kernel<4>
+                                   : moe_pick_kernel<16>;
+    hipLaunchKernelGGL(pick, dim3(a.T), dim3(kWave), 0, stream, a);
+  }
   const int rows = a.T * a.top_k;
   const int experts = a.E < rows ? a.E : rows, max_entries = experts + rows / 16;
-  const Launch gu = plan_launch(experts, max_entries, a.I / 16, a.H, kGuGroup);
+  const Launch gu = plan_launch(experts, max_entries, a.I / 16, a.H);
   if (gu.group > 1)
-    launch_gate_up<F, B, S, 4, kGuGroup>(a, gu, stream);
+    launch_gate_up<F, B, S, 4, kGroup>(a, gu, max_entries, stream);
   else if (gu.nst == 1)
-    launch_gate_up<F, B, S, 1, 1>(a, gu, stream);
+    launch_gate_up<F, B, S, 1, 1>(a, gu, max_entries, stream);
   else if (gu.nst == 2)
-    launch_gate_up<F, B, S, 2, 1>(a, gu, stream);
+    launch_gate_up<F, B, S, 2, 1>(a, gu, max_entries, stream);
   else if (gu.nst == 3)
-    launch_gate_up<F, B, S, 3, 1>(a, gu, stream);
+    launch_gate_up<F, B, S, 3, 1>(a, gu, max_entries, stream);
   else
-    launch_gate_up<F, B, S, 4, 1>(a, gu, stream);
-  const Launch dn = plan_launch(experts, max_entries, a.H / 32, a.I, kDnGroup);
+    launch_gate_up<F, B, S, 4, 1>(a, gu, max_entries, stream);
+  const Launch dn = plan_launch(experts, max_entries, a.H / 32, a.I);
   if (dn.group > 1)
-    launch_down<F, B, S, 4, kDnGroup>(a, dn, max_entries, stream);
+    launch_down<F, B, S, 4, kGroup>(a, dn, max_entries, stream);
   else if (dn.nst == 1)
     launch_down<F, B, S, 1, 1>(a, dn, max_entries, stream);
   else if (dn.nst == 2)

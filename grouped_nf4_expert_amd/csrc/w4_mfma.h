@@ -72,10 +72,6 @@ __device__ __forceinline__ float scale_f32(float s) { return s; }
 __device__ __forceinline__ float scale_f32(uint16_t s) { return bf16_to_f32(s); }
 __device__ __forceinline__ float scale_f32(uint8_t s) { return e8m0_f32(s); }
 
-__device__ __forceinline__ uint32_t widen(float s) { return __float_as_uint(s); }
-__device__ __forceinline__ uint32_t widen(uint16_t s) { return s; }
-__device__ __forceinline__ uint32_t widen(uint8_t s) { return s; }
-
 // Byte address of the i-th 4-byte word kept in the table rows' second halves.
 __device__ __forceinline__ int lds_half(int i) { return (i >> 5) * 256 + 128 + (i & 31) * 4; }
 
@@ -187,79 +183,75 @@ struct RowScale {
   __device__ __forceinline__ int down_field() const { return min(max(exp - 14, 1), 253); }
 };
 
-// A row's scales of one step, as loaded: neighbours share a register.
-template <int N, typename S>
-struct ScaleWords {
-  static constexpr int kWords = (N * (int)sizeof(S) + 3) / 4;
+// A row's scales of one step.
+template <int B, typename S>
+struct ScaleWord {
+  static constexpr int kBlocks = kStep / B;
+  static constexpr int kBytes = kBlocks * (int)sizeof(S);  // 4 or 8, or 2 (one bf16)
+  static constexpr int kWords = (kBytes + 3) / 4;
   uint32_t v[kWords];
-  // Block b's scale, where the words start `late` blocks before the step's
-  // first (see load_weights); what lies past the row's end is 0 or the last
-  // block's.
-  __device__ __forceinline__ float at(int b, int late) const {
-    if constexpr (sizeof(S) == 4) return __uint_as_float(late > 0 ? v[kWords - 1] : v[b]);
-    if constexpr (sizeof(S) == 2) {
-      const uint32_t w = v[0] >> (16 * late);
-      return __uint_as_float((b & 1) ? w & 0xffff0000u : w << 16);
-    }
-    return e8m0_f32((v[0] >> (8 * late) >> (8 * b)) & 255u);
+  __device__ __forceinline__ float at(int b) const {
+    if constexpr (sizeof(S) == 4) return __uint_as_float(v[b]);
+    if constexpr (sizeof(S) == 2)
+      return __uint_as_float((b & 1) ? v[b >> 1] & 0xffff0000u : v[b >> 1] << 16);
+    return e8m0_f32((v[0] >> (8 * b)) & 255u);
   }
 };
-// How many blocks before step c's first its scales are read from.
+
+// Where the scales of step c start in a row: early enough to end with the row.
 template <int B>
-__device__ __forceinline__ int scales_late(int c, int blocks) {
-  return blocks >= kStep / B ? max((c + 1) * (kStep / B) - blocks, 0) : 0;
+__device__ __forceinline__ int scales_first(int c, int blocks) {
+  return min(c * (kStep / B), max(blocks - kStep / B, 0));
 }
 
-// What one step reads of a weight row.
+// A row's scales from block scales_first on, one load whatever their
+// alignment.  `half`: the row is half a step (K = 64) with half the scales.
 template <int B, typename S>
-struct WeightStep {
-  u32x4 codes;
-  ScaleWords<kStep / B, S> scale;
-};
-
-// Step c of the rows at codes + coff and scales + soff (bytes; coff includes
-// the lane group's 16 bytes).  A row has kb bytes and `blocks` scales; past
-// its end a lane reads the step's first bytes again (the activations there
-// are zero), and the step's scales, one load whatever their alignment, start
-// early enough to end with the row.
-template <int B, typename S>
-__device__ __forceinline__ void load_weights(const uint8_t* codes, const char* scales, int c,
-                                             uint32_t coff, uint32_t soff, int g, int kb,
-                                             int blocks, WeightStep<B, S>& w) {
-  constexpr int N = kStep / B;
-  const uint32_t co = c * (kStep / 2) + g * 16 < kb ? coff : coff - (uint32_t)(g * 16);
-  w.codes = __builtin_nontemporal_load(
-      reinterpret_cast<const u32x4*>(codes + c * (kStep / 2) + co));
-  if (blocks >= N) {
-    struct __attribute__((packed, aligned(sizeof(S)))) Words {
-      uint32_t v[N * sizeof(S) / 4 > 0 ? N * sizeof(S) / 4 : 1];
-    };
-    const int first = c * N - scales_late<B>(c, blocks);
-    if constexpr (N * sizeof(S) >= 4) {
-      const Words r = *reinterpret_cast<const Words*>(scales + first * (int)sizeof(S) + soff);
-#pragma unroll
-      for (int i = 0; i < ScaleWords<N, S>::kWords; ++i) w.scale.v[i] = r.v[i];
-    } else {
-      w.scale.v[0] = *reinterpret_cast<const uint16_t*>(scales + first * (int)sizeof(S) + soff);
-    }
-  } else {  // K = 64, half a step: the row's own scales only
-    if constexpr (B == 32 && sizeof(S) == 1)
-      w.scale.v[0] = *reinterpret_cast<const uint16_t*>(scales + soff);
-    else if constexpr (sizeof(S) == 2)
-      w.scale.v[0] = *reinterpret_cast<const uint16_t*>(scales + soff);
-    else
-#pragma unroll
-      for (int i = 0; i < ScaleWords<N, S>::kWords; ++i)
-        w.scale.v[i] = *reinterpret_cast<const uint32_t*>(scales + soff);
+__device__ __forceinline__ void load_scales(const char* base, uint32_t at, bool half,
+                                            ScaleWord<B, S>& w) {
+  typedef ScaleWord<B, S> W;
+  struct __attribute__((packed, aligned(sizeof(S)))) Raw {
+    uint32_t v[W::kWords];
+  };
+  if constexpr (W::kBytes == 2) {
+    w.v[0] = *reinterpret_cast<const uint16_t*>(base + at);
+  } else if (!half) {
+    __builtin_memcpy(&w, reinterpret_cast<const Raw*>(base + at), sizeof(W));
+  } else if constexpr (sizeof(S) == 4) {
+    w.v[0] = w.v[W::kWords - 1] = *reinterpret_cast<const uint32_t*>(base + at);
+  } else {
+    w.v[0] = *reinterpret_cast<const uint16_t*>(base + at);
   }
+}
+// The words moved to step c's first block; what lies past the row's end becomes
+// zero or the last block's (its activations are zero).
+template <int B, typename S>
+__device__ __forceinline__ void align_scales(ScaleWord<B, S>& w, int c, int blocks) {
+  constexpr int N = kStep / B;
+  const int late = c * N - scales_first<B>(c, blocks);
+  if constexpr (sizeof(S) == 4) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w.v[i] = late > 0 ? w.v[N - 1] : w.v[i];
+  } else if constexpr (N > 1) {
+    w.v[0] >>= min(late * (int)sizeof(S) * 8, 31);
+  }
+}
+
+// The 16 bytes of step c of the rows at codes + coff (coff includes the lane
+// group's 16 bytes).  A row has kb bytes; past its end a lane reads the step's
+// first bytes again (the activations there are zero).
+__device__ __forceinline__ u32x4 load_codes(const uint8_t* codes, int c, uint32_t coff, int g,
+                                            int kb) {
+  const uint32_t co = c * (kStep / 2) + g * 16 < kb ? coff : coff - (uint32_t)(g * 16);
+  return __builtin_nontemporal_load(
+      reinterpret_cast<const u32x4*>(codes + c * (kStep / 2) + co));
 }
 
 // acc += (activations of the step) . (weights of the step)^T.
 template <W4 F, int B, typename S>
-__device__ __forceinline__ f32x4 step_mac(const WeightStep<B, S>& w, int late,
+__device__ __forceinline__ f32x4 step_mac(u32x4 d, const ScaleWord<B, S>& scale,
                                           const u32x4 (&x)[4], const char* lut, uint32_t copy,
                                           f32x4 acc) {
-  u32x4 d = w.codes;
   arrange<B>(d);
   constexpr int kPer = B / 32;  // MFMAs of 32 codes per block
 #pragma unroll
@@ -270,7 +262,7 @@ __device__ __forceinline__ f32x4 step_mac(const WeightStep<B, S>& w, int late,
       const int i = b * kPer + j;
       p = mfma16<F>(x[i], decode8<F>(d[i], lut, copy), p);
     }
-    const float s = w.scale.at(b, late);
+    const float s = scale.at(b);
 #pragma unroll
     for (int r = 0; r < 4; ++r) acc[r] = fmaf(s, p[r], acc[r]);
   }
