@@ -118,8 +118,8 @@ constexpr int kLinWaves = 8;
 // every kLinWaves-th step of K and their sums are added in wavefront order.
 template <int B, typename S, bool ZP, int RT>
 __global__ __launch_bounds__(kLinWaves* kWave) void int4_linear_kernel(Int4LinearArgs a) {
-  __shared__ __align__(16) char lut[kLutBytes];
-  __shared__ float red[kLinWaves][RT][256];
+  extern __shared__ __align__(256) char lut[];
+  auto& red = *reinterpret_cast<float (*)[kLinWaves][RT][256]>(lut + kLutBytes);
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   const int g = lane >> 4, col = lane & 15;
   const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * RT;
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(kLinWaves* kWave) void int4_linear_kernel(Int4Linea
       u32x4 x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = load_frag(xrow[t], c * kStep + k_of<B>(g, i), a.K);
-      acc[t] = step_mac_zp<B, ZP>(d, x, lut, copy, acc[t]);
+      acc[t] = step_mac_zp<B, ZP>(d, x, copy, acc[t]);
     }
   }
 #pragma unroll
@@ -171,10 +171,11 @@ void launch_linear_rt(const Int4LinearArgs& a, hipStream_t stream) {
   const unsigned nt = (unsigned)((a.N + 15) / 16);
   const dim3 block(kLinWaves * kWave);
   if (a.M <= 16)
-    hipLaunchKernelGGL((int4_linear_kernel<B, S, ZP, 1>), dim3(nt, 1), block, 0, stream, a);
+    hipLaunchKernelGGL((int4_linear_kernel<B, S, ZP, 1>), dim3(nt, 1), block,
+                       kLutBytes + kLinWaves * 1024, stream, a);
   else
-    hipLaunchKernelGGL((int4_linear_kernel<B, S, ZP, 4>), dim3(nt, (a.M + 63) / 64), block, 0,
-                       stream, a);
+    hipLaunchKernelGGL((int4_linear_kernel<B, S, ZP, 4>), dim3(nt, (a.M + 63) / 64), block,
+                       kLutBytes + kLinWaves * 4096, stream, a);
 }
 
 template <int B, typename S>

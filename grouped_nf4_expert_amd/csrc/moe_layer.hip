@@ -59,7 +59,7 @@ __device__ __forceinline__ Entry read_entry(uint32_t v) {
 // max_entries entries and the call's rows.
 struct Routing {
   uint32_t* entry;
-  float* row_w;       // routing weight of a grouped row
+  float* row_w;       // routing weight of a grouped row, and 0 behind them
   uint8_t* row_tok;   // token of a grouped row
 };
 // What only the routing itself needs (it lies where the table will be).
@@ -258,6 +258,7 @@ __device__ int route_all(const MoeLayerArgs& a, const Routing& L, RouteScratch& 
     L.row_w[row] = R.pick_w[s];
     if (writer) a.slot_rows[s] = row;
   }
+  if (threadIdx.x == 0) L.row_w[a.T * a.top_k] = 0.0f;
   lds_barrier();
   return n_entries;
 }
@@ -394,7 +395,7 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
       t += G;
       if (t == ig.tiles) {
         t = 0;
-        ++j;
+        j = uniform(j + 1);
       }
     }
   };
@@ -452,32 +453,39 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
   // 4 (l / 16) + r).
   u32x4 x[NST][4];
   f32x4 down;
-  const auto load_x = [&](int j, int pass) {
-    const Entry en = read_entry((uint32_t)uniform((int)p.entry(j)));
-    const uint32_t row =
-        (uint32_t)p.row(en.row0 + min(col, en.cnt - 1)) * (uint32_t)K + k_of<B>(g, 0);
-    // Register i of a step lies in a block that is in the row or past it as a
-    // whole (K is a multiple of the block); past it, the row's start is read
-    // and multiplied by zero.
-    const auto inside = [&](int n, int i) {
-      return ((pass * wk + kw) * NST + n) * kStep + (B == 64 ? (i >> 1) * 64 : i * B) < K;
-    };
-    const auto raw = [&](int n, int i) {
-      typename P::Raw v;
+  constexpr bool kKeep = P::kKeepRaw || NST == 1;
+  typename P::Raw keep[kKeep ? NST : 1][4];
+  uint32_t xrow = 0;
+  // Register i of a step lies in a block that is in the row or past it as a
+  // whole (K is a multiple of the block); past it, the row's start is read and
+  // multiplied by zero.
+  const auto inside = [&](int pass, int n, int i) {
+    return ((pass * wk + kw) * NST + n) * kStep + (B == 64 ? (i >> 1) * 64 : i * B) < K;
+  };
+  const auto raw = [&](int pass, int n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       const int k = ((pass * wk + kw) * NST + n) * kStep + (k_of<B>(0, i) - k_of<B>(0, 0));
-      v.load(p.x + (inside(n, i) ? k : 0), row);
-      return v;
-    };
-    typename P::Raw keep[P::kKeepRaw ? NST : 1][4];
+      keep[kKeep ? n : 0][i].load(p.x + (inside(pass, n, i) ? k : 0), xrow);
+    }
+  };
+  const auto issue_x = [&](int j, int pass) {
+    const Entry en = read_entry((uint32_t)uniform((int)p.entry(j)));
+    xrow = (uint32_t)p.row(en.row0 + min(col, en.cnt - 1)) * (uint32_t)K + k_of<B>(g, 0);
+    raw(pass, 0);
+    if constexpr (kKeep)
+#pragma unroll
+      for (int n = 1; n < NST; ++n) raw(pass, n);
+  };
+  const auto take_x = [&](int pass) {
     uint32_t top = 0;
 #pragma unroll
     for (int n = 0; n < NST; ++n) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) keep[P::kKeepRaw ? n : 0][i] = raw(n, i);
+      if (!kKeep && n > 0) raw(pass, n);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t m = keep[P::kKeepRaw ? n : 0][i].max_bits();
-        top = max(top, inside(n, i) ? m : 0u);
+        const uint32_t m = keep[kKeep ? n : 0][i].max_bits();
+        top = max(top, inside(pass, n, i) ? m : 0u);
       }
     }
     top = max(top, (uint32_t)__shfl_xor((int)top, 16, kWave));
@@ -486,24 +494,27 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
     const float up = rs.up();
 #pragma unroll
     for (int n = 0; n < NST; ++n) {
-      if constexpr (!P::kKeepRaw)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) keep[0][i] = raw(n, i);
+      if (!kKeep) raw(pass, n);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        x[n][i] = keep[P::kKeepRaw ? n : 0][i].half(inside(n, i) ? up : 0.0f);
-      if constexpr (!P::kKeepRaw) __builtin_amdgcn_sched_barrier(0);
+        x[n][i] = keep[kKeep ? n : 0][i].half(inside(pass, n, i) ? up : 0.0f);
+      if constexpr (!kKeep) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) down[r] = __shfl(rs.down(), g * 4 + r, kWave);
   };
 
+  // the first activations and scales go ahead of the weights
+  issue_x(cj, 0);
   fetch(0);
   set_item();
+  __builtin_amdgcn_sched_barrier(0);
   u32x4 w[kBufs][2];
 #pragma unroll
   for (int n = 0; n < kAhead; ++n) load(w[n], n % NST);
   fetch(1);
+  __builtin_amdgcn_sched_barrier(0);
+  take_x(0);
   put(0);
   lds_barrier();
   // an item's steps of a pass; `it` is its position within a turn of the loop
@@ -521,7 +532,7 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const Scale sc = *reinterpret_cast<const Scale*>(mine + scale_at<Scale>(n, h * 16));
-        acc[h] = step_mac<F, B, S>(w[q % kBufs][h], sc, x[n], lut, copy, acc[h]);
+        acc[h] = step_mac<F, B, S>(w[q % kBufs][h], sc, x[n], copy, acc[h]);
         // where registers are short, one tile's decode at a time
         if constexpr (G > 1 || F == W4::kMx4 || groups_per_cu(NST, G) > 1)
           __builtin_amdgcn_sched_barrier(0);
@@ -535,7 +546,7 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
   };
   // the wavefronts' sums of an item meet: [wave][tile][register][lane]
   int turn = 0;
-  const auto meet = [&](const f32x4 (&acc)[2], int tile, bool mine) {
+  const auto meet = [&](const f32x4 (&acc)[2], int tile) {
     char* sums = lut + (turn & 1) * kSumBytes;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -544,21 +555,22 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
         *reinterpret_cast<float*>(
             sums + lds_half(((wave * 2 + h) * 4 + r) * kWave) + lds_half(lane) - 128) = acc[h][r];
     lds_barrier();
-    if (mine) p.finish(team, ig.log_wk, turn, cj, tile, sums);
+    p.finish(team, ig.log_wk, cj, tile, sums);
     ++turn;
   };
   if constexpr (G == 1) {
-    load_x(cj, 0);
     for (;;) {
 #pragma unroll
       for (int it = 0; it < kUnroll; ++it) {
         f32x4 acc[2];
         item_steps(it, acc);
-        meet(acc, ct, turn < n_mine);
+        meet(acc, ct);
         if (turn == rounds) return;
         if (turn < n_mine && ++ct == ig.tiles) {
           ct = 0;
-          load_x(++cj, 0);
+          cj = uniform(cj + 1);
+          issue_x(cj, 0);
+          take_x(0);
         }
       }
     }
@@ -568,7 +580,10 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
 #pragma unroll
       for (int it = 0; it < G; ++it) total[it][0] = total[it][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       for (int pass = 0; pass < ig.passes; ++pass) {
-        load_x(cj, pass);
+        if (round + pass > 0) {
+          issue_x(cj, pass);
+          take_x(pass);
+        }
 #pragma unroll
         for (int it = 0; it < G; ++it) {
           f32x4 acc[2];
@@ -579,7 +594,7 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
         }
       }
 #pragma unroll
-      for (int it = 0; it < G; ++it) meet(total[it], ct + it, round < n_mine);
+      for (int it = 0; it < G; ++it) meet(total[it], ct + it);
       if (round + 1 < n_mine) {
         ct += G;
         if (ct == ig.tiles) {
@@ -598,13 +613,21 @@ __device__ __forceinline__ int tile_col(int o) { return o & 15; }
 // The sum of a team's wavefronts, in wavefront order.
 __device__ __forceinline__ float team_sum(const char* sums, int team, int log_wk, int tile, int o) {
   const char* p = sums + lds_half((((team << log_wk) * 2 + tile) << 8) + o);
-  float v = 0.0f;
-  for (int k = 0; k < 1 << log_wk; k += 2) {
-    v += *reinterpret_cast<const float*>(p + k * (512 / 32 * 256));
-    v += *reinterpret_cast<const float*>(p + (k + 1) * (512 / 32 * 256));
-  }
+  const auto at = [p](int k) { return *reinterpret_cast<const float*>(p + k * (512 / 32 * 256)); };
+  float v = at(0) + at(1);
+  if (log_wk > 1) v = v + at(2) + at(3);
+  if (log_wk > 2) v = v + at(4) + at(5) + at(6) + at(7);
   return v;
 }
+
+__device__ __forceinline__ float silu(float g) {  // through exp2 and rcp, a few units of 2^-24
+  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
+}
+
+// The projections' ends (finish).  Every thread takes part and stores, rows an
+// entry does not have to a row kept for them, and a team that has run out of
+// items repeats its last one's: a store in a branch would make the compiler
+// wait for loads in flight that it cannot count.
 
 // gate_up: 16 gate rows and their 16 up rows; SwiGLU, scaled by the row's
 // routing weight (so the sums over a token's experts need no further factor)
@@ -624,40 +647,19 @@ struct GateUp {
   const uint16_t* x;
   __device__ uint32_t entry(int j) const { return L.entry[j]; }
   __device__ int row(int r) const { return L.row_tok[r]; }
-  __device__ void finish(int team, int log_wk, int round, int j, int tile,
-                         const char* sums) const {
+  __device__ void finish(int team, int log_wk, int j, int tile, const char* sums) const {
     const Entry en = read_entry(L.entry[j]);
-    const int n = 64 << log_wk;
-    // 256 outputs; the wavefronts of a wide team take turns
-    for (int o = ((int)threadIdx.x + round * 256) & (n - 1); o < 256; o += n) {
-      const int row = tile_row(o);
-      if (row >= en.cnt) continue;
-      const float gs = team_sum(sums, team, log_wk, 0, o), us = team_sum(sums, team, log_wk, 1, o);
-      a.h[(uint32_t)((en.row0 + row) * a.I + tile * 16 + tile_col(o))] =
-          gs / (1.0f + expf(-gs)) * us * L.row_w[en.row0 + row];
+    // neighbouring lanes hold an output's gate and up
+    for (int i = threadIdx.x & ((64 << log_wk) - 1); i < 512; i += 64 << log_wk) {
+      const int o = i >> 1, row = tile_row(o);
+      const float v = team_sum(sums, team, log_wk, i & 1, o);
+      const float g = __uint_as_float(dpp_u32<0xA0, 0xF>(0u, __float_as_uint(v)));  // even lane's
+      const float u = __uint_as_float(dpp_u32<0xF5, 0xF>(0u, __float_as_uint(v)));  // odd lane's
+      const int r = row < en.cnt ? en.row0 + row : a.T * a.top_k;
+      a.h[(uint32_t)(r * a.I + tile * 16 + tile_col(o))] = silu(g) * u * L.row_w[r];
     }
   }
 };
-
-template <W4 F, int B, typename S, int NST, int G>
-__global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void moe_gate_up_kernel(MoeLayerArgs a, ItemGrid ig,
-                                                               int max_entries) {
-  extern __shared__ __align__(256) char lut[];
-  static_assert(sizeof(RouteScratch) <= kLutBytes, "the routing's scratch lies in the table");
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  char* slds = lut + kLutBytes;
-  Routing L;
-  L.entry = reinterpret_cast<uint32_t*>(slds + 2 * scale_bytes<ScaleWord<B, S>>(NST));
-  L.row_w = reinterpret_cast<float*>(L.entry + max_entries);
-  L.row_tok = reinterpret_cast<uint8_t*>(L.row_w + a.T * a.top_k);
-  const int n_entries =
-      route_all(a, L, *reinterpret_cast<RouteScratch*>(lut), wave, lane, blockIdx.x == 0);
-  fill_lut<F>(lut);
-  lds_barrier();
-  const GateUp<S> p = {a, L, a.gu_packed, static_cast<const S*>(a.gu_scales),
-                       2 * (size_t)a.I, a.I, a.x};
-  expert_tiles<F, B, S, NST, G>(p, ig, n_entries, lut, slds);
-}
 
 // down: 32 weight rows, fp32 sums per grouped row.
 template <typename S>
@@ -674,18 +676,35 @@ struct Down {
   const float* x;
   __device__ uint32_t entry(int j) const { return entries[j]; }
   __device__ int row(int r) const { return r; }
-  __device__ void finish(int team, int log_wk, int round, int j, int tile,
-                         const char* sums) const {
+  __device__ void finish(int team, int log_wk, int j, int tile, const char* sums) const {
     const Entry en = read_entry(entries[j]);
-    const int n = 64 << log_wk;
-    for (int i = ((int)threadIdx.x + round * 512) & (n - 1); i < 512; i += n) {
+    for (int i = threadIdx.x & ((64 << log_wk) - 1); i < 512; i += 64 << log_wk) {
       const int h = i >> 8, o = i & 255, row = tile_row(o);
-      if (row < en.cnt)
-        a.y[(size_t)(en.row0 + row) * a.H + tile * 32 + h * 16 + tile_col(o)] =
-            team_sum(sums, team, log_wk, h, o);
+      const int r = row < en.cnt ? en.row0 + row : a.T * a.top_k;
+      a.y[(size_t)r * a.H + tile * 32 + h * 16 + tile_col(o)] = team_sum(sums, team, log_wk, h, o);
     }
   }
 };
+
+template <W4 F, int B, typename S, int NST, int G>
+__global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void moe_gate_up_kernel(MoeLayerArgs a, ItemGrid ig,
+                                                               int max_entries) {
+  extern __shared__ __align__(256) char lut[];
+  static_assert(sizeof(RouteScratch) <= kLutBytes, "the routing's scratch lies in the table");
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  char* slds = lut + kLutBytes;
+  Routing L;
+  L.entry = reinterpret_cast<uint32_t*>(slds + 2 * scale_bytes<ScaleWord<B, S>>(NST));
+  L.row_w = reinterpret_cast<float*>(L.entry + max_entries);
+  L.row_tok = reinterpret_cast<uint8_t*>(L.row_w + a.T * a.top_k + 1);
+  const int n_entries =
+      route_all(a, L, *reinterpret_cast<RouteScratch*>(lut), wave, lane, blockIdx.x == 0);
+  fill_lut<F>(lut);
+  lds_barrier();
+  const GateUp<S> p = {a, L, a.gu_packed, static_cast<const S*>(a.gu_scales),
+                       2 * (size_t)a.I, a.I, a.x};
+  expert_tiles<F, B, S, NST, G>(p, ig, n_entries, lut, slds);
+}
 
 template <W4 F, int B, typename S, int NST, int G>
 __global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void moe_down_kernel(MoeLayerArgs a, ItemGrid ig,
@@ -761,7 +780,7 @@ Launch plan_launch(int entries, int max_entries, int tiles, int K) {
 template <W4 F, int B, typename S, int NST, int G>
 void launch_gate_up(const MoeLayerArgs& a, const Launch& l, int max_entries, hipStream_t stream) {
   const int lds = kLutBytes + 2 * scale_bytes<ScaleWord<B, S>>(NST) + 4 * max_entries +
-                  5 * a.T * a.top_k;
+                  4 + 5 * a.T * a.top_k;
   hipLaunchKernelGGL((moe_gate_up_kernel<F, B, S, NST, G>), dim3(l.grid), dim3(kThreads), lds,
                      stream, a, l.ig, max_entries);
 }

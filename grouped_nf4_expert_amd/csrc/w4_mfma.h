@@ -76,7 +76,9 @@ __device__ __forceinline__ float scale_f32(uint8_t s) { return e8m0_f32(s); }
 __device__ __forceinline__ int lds_half(int i) { return (i >> 5) * 256 + 128 + (i & 31) * 4; }
 
 // The decode table, filled by the whole workgroup (a barrier must follow).
-// Thread t writes half of entry t / 2.
+// Thread t writes half of entry t / 2.  decode8 reads it at LDS address 0: it
+// is the first thing of the workgroup's dynamic LDS, and its kernels have no
+// static LDS.
 template <W4 F>
 __device__ __forceinline__ void fill_lut(char* lut) {
   if constexpr (F != W4::kMx4) {
@@ -107,7 +109,7 @@ __device__ __forceinline__ void fill_lut(char* lut) {
 // Eight codes of one dword as an MFMA operand, in k order: bf16 for int4,
 // fp16 for the others.
 template <W4 F>
-__device__ __forceinline__ u32x4 decode8(uint32_t w, const char* lut, uint32_t copy) {
+__device__ __forceinline__ u32x4 decode8(uint32_t w, uint32_t copy) {
   if constexpr (F == W4::kMx4) {
     const half2v p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
     const half2v p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
@@ -116,8 +118,11 @@ __device__ __forceinline__ u32x4 decode8(uint32_t w, const char* lut, uint32_t c
     return u32x4{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1),
                  __builtin_bit_cast(uint32_t, p2), __builtin_bit_cast(uint32_t, p3)};
   } else {
-    // address: the byte in bits 8..15, this lane's copy in bits 0..7
-    const auto at = [lut](uint32_t addr) { return *reinterpret_cast<const uint32_t*>(lut + addr); };
+    // address: the byte in bits 8..15, this lane's copy in bits 0..7 (the
+    // table lies at LDS address 0)
+    const auto at = [](uint32_t addr) {
+      return *(const __attribute__((address_space(3))) uint32_t*)addr;
+    };
     return u32x4{at(__builtin_amdgcn_perm(w, copy, 0x0c0c0400u)),
                  at(__builtin_amdgcn_perm(w, copy, 0x0c0c0500u)),
                  at(__builtin_amdgcn_perm(w, copy, 0x0c0c0600u)),
@@ -250,8 +255,7 @@ __device__ __forceinline__ u32x4 load_codes(const uint8_t* codes, int c, uint32_
 // acc += (activations of the step) . (weights of the step)^T.
 template <W4 F, int B, typename S>
 __device__ __forceinline__ f32x4 step_mac(u32x4 d, const ScaleWord<B, S>& scale,
-                                          const u32x4 (&x)[4], const char* lut, uint32_t copy,
-                                          f32x4 acc) {
+                                          const u32x4 (&x)[4], uint32_t copy, f32x4 acc) {
   arrange<B>(d);
   constexpr int kPer = B / 32;  // MFMAs of 32 codes per block
 #pragma unroll
@@ -260,7 +264,7 @@ __device__ __forceinline__ f32x4 step_mac(u32x4 d, const ScaleWord<B, S>& scale,
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = b * kPer + j;
-      p = mfma16<F>(x[i], decode8<F>(d[i], lut, copy), p);
+      p = mfma16<F>(x[i], decode8<F>(d[i], copy), p);
     }
     const float s = scale.at(b);
 #pragma unroll
@@ -310,7 +314,7 @@ __device__ __forceinline__ u32x4 load_frag(const uint16_t* row, int k, int K) {
 
 template <int B, bool ZP, typename S>
 __device__ __forceinline__ f32x4 step_mac_zp(StepData<B, S> d, const u32x4 (&x)[4],
-                                          const char* lut, uint32_t copy, f32x4 acc) {
+                                             uint32_t copy, f32x4 acc) {
   arrange<B>(d.codes);
   constexpr int kPer = B / 32;  // MFMAs of 32 codes per block
 #pragma unroll
@@ -319,7 +323,7 @@ __device__ __forceinline__ f32x4 step_mac_zp(StepData<B, S> d, const u32x4 (&x)[
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = b * kPer + j;
-      p = mfma16<W4::kInt4>(x[i], decode8<W4::kInt4>(d.codes[i], lut, copy), p);
+      p = mfma16<W4::kInt4>(x[i], decode8<W4::kInt4>(d.codes[i], copy), p);
       if constexpr (ZP) {  // (q - 8) - (z - 8), both exact in bf16
         const uint32_t z = pack_bf16x2((float)(8 - (int)d.zero[b]), (float)(8 - (int)d.zero[b]));
         p = mfma16<W4::kInt4>(x[i], u32x4{z, z, z, z}, p);
