@@ -168,9 +168,8 @@ static MoeLayerRegions moe_layer_regions(int64_t T, int32_t top_k, int64_t H, in
   const size_t rows = (size_t)T * top_k;
   r.entries = take((1 + kMoeLayerMaxEntries) * sizeof(uint32_t));
   r.slot_rows = take(rows * sizeof(int32_t));
-  // one row more than the call's: where the kernels put rows that are none
-  r.h = take((rows + 1) * I * sizeof(float));
-  r.y = take((rows + 1) * H * sizeof(float));
+  r.h = take(rows * I * sizeof(float));
+  r.y = take(rows * H * sizeof(float));
   r.total = at;
   return r;
 }

@@ -368,8 +368,8 @@ struct MoeLayerArgs {
   float* topk_w;              // [T, top_k]
   uint32_t* entries;          // the number of entries, then the entries
   int32_t* slot_rows;         // [T * top_k]: grouped row of each slot
-  float* h;                   // [T * top_k + 1, I]: routing weight x SwiGLU
-  float* y;                   // [T * top_k + 1, H]: the down projection's rows
+  float* h;                   // [T * top_k, I]: routing weight x SwiGLU
+  float* y;                   // [T * top_k, H]: the down projection's rows
   int T, E, top_k, H, I;
 };
 hipError_t launch_moe_layer(const MoeLayerArgs& a, int scale_kind, hipStream_t stream);

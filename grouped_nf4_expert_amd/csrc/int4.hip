@@ -1,6 +1,6 @@
 // int4 weights with group scales: the packer and the linear layer over it.
 
-#include "w4_mfma.h"
+#include "w4_tiles.h"
 
 namespace gnf4 {
 namespace {
@@ -111,71 +111,218 @@ void launch_pack_s(const Int4PackArgs& a, unsigned grid, hipStream_t stream) {
 }
 
 // -------------------------------------------------------------- int4_linear
+//
+// Up to 16 rows of activations: the weight stream bounds it, and the loop of
+// w4_tiles.h runs over one entry (the rows) and the matrix's 32-row tiles.
 
-constexpr int kLinWaves = 8;
-
-// One workgroup per 16 output columns and 16 RT rows; its wavefronts take
-// every kLinWaves-th step of K and their sums are added in wavefront order.
-template <int B, typename S, bool ZP, int RT>
-__global__ __launch_bounds__(kLinWaves* kWave) void int4_linear_kernel(Int4LinearArgs a) {
-  extern __shared__ __align__(256) char lut[];
-  auto& red = *reinterpret_cast<float (*)[kLinWaves][RT][256]>(lut + kLutBytes);
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  const int g = lane >> 4, col = lane & 15;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * RT;
-  const int n = min(n0 + col, a.N - 1);
-  const int blocks = a.K / B;
-  const WeightRow<S> w = {a.packed + (size_t)n * (a.K / 2),
-                          static_cast<const S*>(a.scales) + (size_t)n * blocks,
-                          ZP ? a.zeros + (size_t)n * blocks : nullptr};
-  const uint16_t* xrow[RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t)
-    xrow[t] = a.x + (size_t)min(m0 + t * 16 + col, a.M - 1) * a.K;
-  fill_lut<W4::kInt4>(lut);
-  __syncthreads();
-  const uint32_t copy = lut_copy(lane);
-  f32x4 acc[RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int steps = (a.K + kStep - 1) / kStep;
-  for (int c = wave; c < steps; c += kLinWaves) {
-    StepData<B, S> d;
-    load_step<B, ZP>(w, c, g, a.K, d);
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      u32x4 x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = load_frag(xrow[t], c * kStep + k_of<B>(g, i), a.K);
-      acc[t] = step_mac_zp<B, ZP>(d, x, copy, acc[t]);
+template <typename S>
+struct Rows {
+  typedef RawBf16 Raw;
+  static constexpr bool kKeepRaw = true;
+  static constexpr int second = 16;
+  const Int4LinearArgs& a;
+  const uint8_t* codes;
+  const S* scales;
+  const uint8_t* zeros;
+  const uint16_t* x;
+  int max_row;  // the last row of a tile that the matrix has
+  static constexpr size_t expert_rows = 0;
+  __device__ uint32_t entry(int) const { return make_entry(0, 0, a.M); }
+  __device__ int row(int r) const { return r; }
+  // the last tile ends with the matrix, over rows of the tile before it
+  __device__ int first_row(int tile) const { return min(tile * 32, max(a.N - 32, 0)); }
+  __device__ void finish(int team, int log_wk, int, int tile, const char* sums) const {
+    const int n0 = first_row(tile);
+    for (int i = threadIdx.x & ((64 << log_wk) - 1); i < 512; i += 64 << log_wk) {
+      const int h = i >> 8, o = i & 255;
+      const int n = min(n0 + h * 16 + tile_col(o), a.N - 1);
+      float y = team_sum(sums, team, log_wk, h, o);
+      if (a.bias) y += bf16_to_f32(a.bias[n]);
+      a.y[(size_t)min(tile_row(o), a.M - 1) * a.N + n] = f32_to_bf16(y);
     }
   }
+};
+
+template <int B, typename S, bool ZP, int NST, int G>
+__global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void int4_rows_kernel(
+    Int4LinearArgs a, ItemGrid ig) {
+  extern __shared__ __align__(256) char lut[];
+  fill_lut<W4::kInt4>(lut);
+  lds_barrier();
+  const Rows<S> p = {a, a.packed, static_cast<const S*>(a.scales), a.zeros, a.x,
+                     min(a.N, 32) - 1};
+  expert_tiles<W4::kInt4, B, S, ZP, NST, G>(p, ig, 1, lut, lut + kLutBytes);
+}
+
+template <int B, typename S, bool ZP, int NST, int G>
+void launch_rows_n(const Int4LinearArgs& a, const Launch& l, hipStream_t stream) {
+  const int lds = kLutBytes + 2 * scale_bytes<ScaleWord<B, S, ZP>>(NST);
+  hipLaunchKernelGGL((int4_rows_kernel<B, S, ZP, NST, G>), dim3(l.grid), dim3(kThreads), lds,
+                     stream, a, l.ig);
+}
+
+constexpr int kRowsGroup = 2;
+
+template <int B, typename S, bool ZP>
+void launch_rows(const Int4LinearArgs& a, hipStream_t stream) {
+  const int tiles = (a.N + 31) / 32;
+  Launch l = plan_launch(1, 1, tiles, a.K, kRowsGroup);
+  l.ig.tiles = (tiles + l.group - 1) / l.group * l.group;
+  if (l.group > 1)
+    launch_rows_n<B, S, ZP, 4, kRowsGroup>(a, l, stream);
+  else if (l.nst == 1)
+    launch_rows_n<B, S, ZP, 1, 1>(a, l, stream);
+  else if (l.nst == 2)
+    launch_rows_n<B, S, ZP, 2, 1>(a, l, stream);
+  else if (l.nst == 3)
+    launch_rows_n<B, S, ZP, 3, 1>(a, l, stream);
+  else
+    launch_rows_n<B, S, ZP, 4, 1>(a, l, stream);
+}
+
+// More rows: a wavefront holds 16 RT rows x 64 columns of the product, so a
+// decoded operand serves RT products and an activation fragment four, and the
+// eight wavefronts of a workgroup split the steps of K; their sums meet in LDS,
+// in wavefront order.
+constexpr int kGemmCols = 4;  // column tiles of 16
+
+template <int B, typename S, bool ZP, int RT>
+__global__ __launch_bounds__(kThreads) void int4_gemm_kernel(Int4LinearArgs a) {
+  typedef ScaleWord<B, S, ZP> Scale;
+  extern __shared__ __align__(256) char lut[];
+  fill_lut<W4::kInt4>(lut);
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const int g = lane >> 4, col = lane & 15;
+  const int n0 = blockIdx.x * 64, m0 = blockIdx.y * 16 * RT;
+  const int kb = a.K / 2, blocks = a.K / B, steps = (a.K + kStep - 1) / kStep;
+  const uint32_t copy = lut_copy(lane);
+  size_t wrow[kGemmCols];
 #pragma unroll
-  for (int t = 0; t < RT; ++t)
+  for (int t = 0; t < kGemmCols; ++t) wrow[t] = min(n0 + t * 16 + col, a.N - 1);
+  const uint16_t* xrow[RT];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) red[wave][t][(g * 4 + r) * 16 + col] = acc[t][r];
-  __syncthreads();
-  for (int i = threadIdx.x; i < RT * 256; i += kLinWaves * kWave) {
-    const int m = m0 + (i >> 4), nn = n0 + (i & 15);
-    if (m >= a.M || nn >= a.N) continue;
-    float y = 0.0f;
+  for (int t = 0; t < RT; ++t) xrow[t] = a.x + (size_t)min(m0 + t * 16 + col, a.M - 1) * a.K;
+  f32x4 acc[kGemmCols][RT];
 #pragma unroll
-    for (int k = 0; k < kLinWaves; ++k) y += red[k][i >> 8][i & 255];
-    if (a.bias) y += bf16_to_f32(a.bias[nn]);
-    a.y[(size_t)m * a.N + nn] = f32_to_bf16(y);
+  for (int t = 0; t < kGemmCols; ++t)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[t][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  u32x4 w[kGemmCols], wn[kGemmCols];
+  Scale sc[kGemmCols], scn[kGemmCols];
+  const auto load = [&](int c, u32x4 (&d)[kGemmCols], Scale (&s)[kGemmCols]) {
+#pragma unroll
+    for (int t = 0; t < kGemmCols; ++t) {
+      d[t] = load_codes(a.packed + wrow[t] * kb, c, (uint32_t)(g * 16), g, kb);
+      load_scales<B, S, ZP, true>(static_cast<const S*>(a.scales) + wrow[t] * blocks,
+                                  ZP ? a.zeros + wrow[t] * blocks : nullptr,
+                                  (uint32_t)scales_first<B>(c, blocks), blocks, s[t]);
+    }
+  };
+  load(min(wave, steps - 1), wn, scn);
+  lds_barrier();
+  for (int c = wave; c < steps; c += kWaves) {
+#pragma unroll
+    for (int t = 0; t < kGemmCols; ++t) {
+      w[t] = wn[t];
+      sc[t] = scn[t];
+    }
+    u32x4 x[RT][4];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = c * kStep + k_of<B>(g, i);
+        x[r][i] = *reinterpret_cast<const u32x4*>(xrow[r] + (k < a.K ? k : 0));
+      }
+    load(min(c + kWaves, steps - 1), wn, scn);
+    if ((c + 1) * kStep > a.K)  // the row's end: zero activations past it
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c * kStep + k_of<B>(g, i) >= a.K) x[r][i] = u32x4{0u, 0u, 0u, 0u};
+    constexpr int kPer = B / 32;
+    // the activations' sums over each block, for the zero points
+    f32x4 sum[ZP ? kStep / B : 1][ZP ? RT : 1];
+    if constexpr (ZP) {
+#pragma unroll
+      for (int b = 0; b < kStep / B; ++b)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int j = 0; j < kPer; ++j)
+            p = mfma16<W4::kInt4>(x[r][b * kPer + j],
+                                  u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}, p);
+          sum[b][r] = p;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kGemmCols; ++t) {
+      align_scales<B, S, ZP>(sc[t], c, blocks);
+      arrange<B>(w[t]);
+#pragma unroll
+      for (int b = 0; b < kStep / B; ++b) {
+        f32x4 p[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) p[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const u32x4 d = decode8<W4::kInt4>(w[t][b * kPer + j], copy);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) p[r] = mfma16<W4::kInt4>(x[r][b * kPer + j], d, p[r]);
+        }
+        const float s = sc[t].at(b);
+        const float z = ZP ? (float)(8 - sc[t].zero(b)) : 0.0f;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if constexpr (ZP) p[r][q] = fmaf(z, sum[b][r][q], p[r][q]);
+            acc[t][r][q] = fmaf(s, p[r][q], acc[t][r][q]);
+          }
+      }
+    }
   }
+  lds_barrier();  // the table has been read; the sums take its place
+  // one column tile at a time: [wave][row tile][register][lane]
+  float* red = reinterpret_cast<float*>(lut);
+#pragma unroll
+  for (int t = 0; t < kGemmCols; ++t) {
+    float* set = red + (t & 1) * (kWaves * RT * 256);
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) set[((wave * RT + r) * 4 + q) * kWave + lane] = acc[t][r][q];
+    lds_barrier();
+    for (int i = threadIdx.x; i < RT * 256; i += kThreads) {
+      const int m = m0 + (i >> 8) * 16 + tile_row(i & 255), n = n0 + t * 16 + tile_col(i & 255);
+      float y = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) y += set[k * RT * 256 + i];
+      if (m < a.M && n < a.N) {
+        if (a.bias) y += bf16_to_f32(a.bias[n]);
+        a.y[(size_t)m * a.N + n] = f32_to_bf16(y);
+      }
+    }
+  }
+}
+
+template <int B, typename S, bool ZP, int RT>
+void launch_gemm(const Int4LinearArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL((int4_gemm_kernel<B, S, ZP, RT>),
+                     dim3((a.N + 63) / 64, (a.M + 16 * RT - 1) / (16 * RT)), dim3(kThreads),
+                     kLutBytes, stream, a);
 }
 
 template <int B, typename S, bool ZP>
 void launch_linear_rt(const Int4LinearArgs& a, hipStream_t stream) {
-  const unsigned nt = (unsigned)((a.N + 15) / 16);
-  const dim3 block(kLinWaves * kWave);
   if (a.M <= 16)
-    hipLaunchKernelGGL((int4_linear_kernel<B, S, ZP, 1>), dim3(nt, 1), block,
-                       kLutBytes + kLinWaves * 1024, stream, a);
+    launch_rows<B, S, ZP>(a, stream);
+  else if (a.M <= 32)
+    launch_gemm<B, S, ZP, 2>(a, stream);
   else
-    hipLaunchKernelGGL((int4_linear_kernel<B, S, ZP, 4>), dim3(nt, (a.M + 63) / 64), block,
-                       kLutBytes + kLinWaves * 4096, stream, a);
+    launch_gemm<B, S, ZP, 4>(a, stream);
 }
 
 template <int B, typename S>

@@ -188,19 +188,20 @@ struct RowScale {
   __device__ __forceinline__ int down_field() const { return min(max(exp - 14, 1), 253); }
 };
 
-// A row's scales of one step.
-template <int B, typename S>
+// A row's scales of one step, and its zero points (bytes) where the format has
+// them.
+template <int B, typename S, bool ZP>
 struct ScaleWord {
   static constexpr int kBlocks = kStep / B;
-  static constexpr int kBytes = kBlocks * (int)sizeof(S);  // 4 or 8, or 2 (one bf16)
-  static constexpr int kWords = (kBytes + 3) / 4;
-  uint32_t v[kWords];
+  static constexpr int kWords = (kBlocks * (int)sizeof(S) + 3) / 4;
+  uint32_t v[kWords + (ZP ? 1 : 0)];
   __device__ __forceinline__ float at(int b) const {
     if constexpr (sizeof(S) == 4) return __uint_as_float(v[b]);
     if constexpr (sizeof(S) == 2)
       return __uint_as_float((b & 1) ? v[b >> 1] & 0xffff0000u : v[b >> 1] << 16);
     return e8m0_f32((v[0] >> (8 * b)) & 255u);
   }
+  __device__ __forceinline__ int zero(int b) const { return (int)(v[kWords] >> (8 * b)) & 255; }
 };
 
 // Where the scales of step c start in a row: early enough to end with the row.
@@ -209,36 +210,71 @@ __device__ __forceinline__ int scales_first(int c, int blocks) {
   return min(c * (kStep / B), max(blocks - kStep / B, 0));
 }
 
-// A row's scales from block scales_first on, one load whatever their
-// alignment.  `half`: the row is half a step (K = 64) with half the scales.
-template <int B, typename S>
-__device__ __forceinline__ void load_scales(const char* base, uint32_t at, bool half,
-                                            ScaleWord<B, S>& w) {
-  typedef ScaleWord<B, S> W;
-  struct __attribute__((packed, aligned(sizeof(S)))) Raw {
-    uint32_t v[W::kWords];
-  };
-  if constexpr (W::kBytes == 2) {
-    w.v[0] = *reinterpret_cast<const uint16_t*>(base + at);
-  } else if (!half) {
-    __builtin_memcpy(&w, reinterpret_cast<const Raw*>(base + at), sizeof(W));
-  } else if constexpr (sizeof(S) == 4) {
-    w.v[0] = w.v[W::kWords - 1] = *reinterpret_cast<const uint32_t*>(base + at);
+// N neighbouring elements of E bytes, whatever their alignment, as words.
+template <int N, int E>
+__device__ __forceinline__ void load_run(const void* p, uint32_t* v) {
+  if constexpr (N * E == 1) {
+    v[0] = *static_cast<const uint8_t*>(p);
+  } else if constexpr (N * E == 2) {
+    struct __attribute__((packed, aligned(E))) Raw {
+      uint16_t v;
+    };
+    v[0] = static_cast<const Raw*>(p)->v;
   } else {
-    w.v[0] = *reinterpret_cast<const uint16_t*>(base + at);
+    struct __attribute__((packed, aligned(E))) Raw {
+      uint32_t v[N * E / 4];
+    };
+    const Raw r = *static_cast<const Raw*>(p);
+#pragma unroll
+    for (int i = 0; i < N * E / 4; ++i) v[i] = r.v[i];
   }
 }
-// The words moved to step c's first block; what lies past the row's end becomes
-// zero or the last block's (its activations are zero).
-template <int B, typename S>
-__device__ __forceinline__ void align_scales(ScaleWord<B, S>& w, int c, int blocks) {
-  constexpr int N = kStep / B;
-  const int late = c * N - scales_first<B>(c, blocks);
-  if constexpr (sizeof(S) == 4) {
+
+// A row's scales (and zero points) from element `at` on.  SHORT: the row may
+// have fewer blocks than a step; then one load per block it has.
+template <int B, typename S, bool ZP, bool SHORT>
+__device__ __forceinline__ void load_scales(const S* scales, const uint8_t* zeros, uint32_t at,
+                                            int blocks, ScaleWord<B, S, ZP>& w) {
+  typedef ScaleWord<B, S, ZP> W;
+  constexpr int N = W::kBlocks;
+  if (SHORT && blocks < N) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) w.v[i] = late > 0 ? w.v[N - 1] : w.v[i];
-  } else if constexpr (N > 1) {
-    w.v[0] >>= min(late * (int)sizeof(S) * 8, 31);
+    for (int i = 0; i < W::kWords + (ZP ? 1 : 0); ++i) w.v[i] = 0u;
+#pragma unroll
+    for (int b = 0; b < N - 1; ++b) {
+      if (b >= blocks) break;
+      uint32_t e;
+      load_run<1, (int)sizeof(S)>(scales + at + b, &e);
+      w.v[b * sizeof(S) / 4] |= e << (b * sizeof(S) % 4 * 8);
+      if constexpr (ZP) w.v[W::kWords] |= (uint32_t)zeros[at + b] << (8 * b);
+    }
+    return;
+  }
+  load_run<N, (int)sizeof(S)>(reinterpret_cast<const char*>(scales) + at * (uint32_t)sizeof(S), w.v);
+  if constexpr (ZP) load_run<N, 1>(zeros + at, w.v + W::kWords);
+}
+// The words moved to step c's first block; what lies past the row's end becomes
+// zero or a block of the row's (its activations are zero).
+template <int B, typename S, bool ZP>
+__device__ __forceinline__ void align_scales(ScaleWord<B, S, ZP>& w, int c, int blocks) {
+  typedef ScaleWord<B, S, ZP> W;
+  constexpr int N = W::kBlocks;
+  if constexpr (N > 1) {
+    const int late = c * N - scales_first<B>(c, blocks);  // 0 but in a row's last step
+    if constexpr (sizeof(S) == 4) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int l = 1; l < N; ++l) w.v[i] = late == l ? w.v[min(i + l, N - 1)] : w.v[i];
+      }
+    } else if constexpr (W::kWords == 2) {
+      const uint64_t v = (((uint64_t)w.v[1] << 32) | w.v[0]) >> (16 * late);
+      w.v[0] = (uint32_t)v;
+      w.v[1] = (uint32_t)(v >> 32);
+    } else {
+      w.v[0] >>= late * (int)sizeof(S) * 8;
+    }
+    if constexpr (ZP) w.v[W::kWords] >>= 8 * late;
   }
 }
 
@@ -253,83 +289,25 @@ __device__ __forceinline__ u32x4 load_codes(const uint8_t* codes, int c, uint32_
 }
 
 // acc += (activations of the step) . (weights of the step)^T.
-template <W4 F, int B, typename S>
-__device__ __forceinline__ f32x4 step_mac(u32x4 d, const ScaleWord<B, S>& scale,
+template <W4 F, int B, typename S, bool ZP>
+__device__ __forceinline__ f32x4 step_mac(u32x4 d, const ScaleWord<B, S, ZP>& scale,
                                           const u32x4 (&x)[4], uint32_t copy, f32x4 acc) {
   arrange<B>(d);
   constexpr int kPer = B / 32;  // MFMAs of 32 codes per block
 #pragma unroll
   for (int b = 0; b < kStep / B; ++b) {
     f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t z = 0u;
+    if constexpr (ZP) z = pack_bf16x2((float)(8 - scale.zero(b)), (float)(8 - scale.zero(b)));
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = b * kPer + j;
       p = mfma16<F>(x[i], decode8<F>(d[i], copy), p);
+      // the codes' pairs are q - 8: a zero point adds (8 - z) times the sum of
+      // the activations, both exact in bf16
+      if constexpr (ZP) p = mfma16<F>(x[i], u32x4{z, z, z, z}, p);
     }
     const float s = scale.at(b);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) acc[r] = fmaf(s, p[r], acc[r]);
-  }
-  return acc;
-}
-
-// One lane's weight row: codes, scales and (int4) zero points, all of the
-// row's K.
-template <typename S>
-struct WeightRow {
-  const uint8_t* codes;
-  const S* scales;
-  const uint8_t* zeros;
-};
-
-// What one step reads of a weight row.
-template <int B, typename S>
-struct StepData {
-  u32x4 codes;
-  S scale[kStep / B];
-  uint8_t zero[kStep / B];
-};
-
-// Step c of a row of K codes.  Past the end of the row a lane reads the row's
-// start again and the last block's scale: the activations there are zero.
-template <int B, bool ZP, typename S>
-__device__ __forceinline__ void load_step(const WeightRow<S>& w, int c, int g, int K,
-                                          StepData<B, S>& d) {
-  const int off = c * (kStep / 2) + g * 16;
-  d.codes = *reinterpret_cast<const u32x4*>(w.codes + (off < K / 2 ? off : 0));
-#pragma unroll
-  for (int b = 0; b < kStep / B; ++b) {
-    const int blk = min(c * (kStep / B) + b, K / B - 1);
-    d.scale[b] = w.scales[blk];
-    if constexpr (ZP) d.zero[b] = w.zeros[blk];
-  }
-}
-
-// Eight activations of one row at k, or zeros past the row's end.
-__device__ __forceinline__ u32x4 load_frag(const uint16_t* row, int k, int K) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (k < K) v = *reinterpret_cast<const u32x4*>(row + k);
-  return v;
-}
-
-template <int B, bool ZP, typename S>
-__device__ __forceinline__ f32x4 step_mac_zp(StepData<B, S> d, const u32x4 (&x)[4],
-                                             uint32_t copy, f32x4 acc) {
-  arrange<B>(d.codes);
-  constexpr int kPer = B / 32;  // MFMAs of 32 codes per block
-#pragma unroll
-  for (int b = 0; b < kStep / B; ++b) {
-    f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = b * kPer + j;
-      p = mfma16<W4::kInt4>(x[i], decode8<W4::kInt4>(d.codes[i], copy), p);
-      if constexpr (ZP) {  // (q - 8) - (z - 8), both exact in bf16
-        const uint32_t z = pack_bf16x2((float)(8 - (int)d.zero[b]), (float)(8 - (int)d.zero[b]));
-        p = mfma16<W4::kInt4>(x[i], u32x4{z, z, z, z}, p);
-      }
-    }
-    const float s = scale_f32(d.scale[b]);
 #pragma unroll
     for (int r = 0; r < 4; ++r) acc[r] = fmaf(s, p[r], acc[r]);
   }
