@@ -115,69 +115,86 @@ void launch_pack_s(const Int4PackArgs& a, unsigned grid, hipStream_t stream) {
 // Up to 16 rows of activations: the weight stream bounds it, and the loop of
 // w4_tiles.h runs over one entry (the rows) and the matrix's 32-row tiles.
 
-template <typename S>
+template <typename S, int U>
 struct Rows {
   typedef RawBf16 Raw;
   static constexpr bool kKeepRaw = true;
-  static constexpr int second = 16;
+  static constexpr int second = 16, kRows = 16 * U;
   const Int4LinearArgs& a;
   const uint8_t* codes;
   const S* scales;
   const uint8_t* zeros;
   const uint16_t* x;
-  int max_row;  // the last row of a tile that the matrix has
+  int max_row;  // the last row of an item that the matrix has
   static constexpr size_t expert_rows = 0;
   __device__ uint32_t entry(int) const { return make_entry(0, 0, a.M); }
   __device__ int row(int r) const { return r; }
-  // the last tile ends with the matrix, over rows of the tile before it
-  __device__ int first_row(int tile) const { return min(tile * 32, max(a.N - 32, 0)); }
-  __device__ void finish(int team, int log_wk, int, int tile, const char* sums) const {
-    const int n0 = first_row(tile);
-    for (int i = threadIdx.x & ((64 << log_wk) - 1); i < 512; i += 64 << log_wk) {
+  // the last item ends with the matrix, over rows of the item before it
+  __device__ int first_row(int item) const { return min(item * kRows, max(a.N - kRows, 0)); }
+  __device__ void finish(int team, int log_wk, int, int item, const char* sums) const {
+    const int n0 = first_row(item);
+    for (int i = threadIdx.x & ((64 << log_wk) - 1); i < U * 256; i += 64 << log_wk) {
       const int h = i >> 8, o = i & 255;
       const int n = min(n0 + h * 16 + tile_col(o), a.N - 1);
-      float y = team_sum(sums, team, log_wk, h, o);
+      float y = team_sum<U>(sums, team, log_wk, h, o);
       if (a.bias) y += bf16_to_f32(a.bias[n]);
       a.y[(size_t)min(tile_row(o), a.M - 1) * a.N + n] = f32_to_bf16(y);
     }
   }
 };
 
-template <int B, typename S, bool ZP, int NST, int G>
+template <int B, typename S, bool ZP, int NST, int G, int U>
 __global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void int4_rows_kernel(
     Int4LinearArgs a, ItemGrid ig) {
   extern __shared__ __align__(256) char lut[];
   fill_lut<W4::kInt4>(lut);
   lds_barrier();
-  const Rows<S> p = {a, a.packed, static_cast<const S*>(a.scales), a.zeros, a.x,
-                     min(a.N, 32) - 1};
-  expert_tiles<W4::kInt4, B, S, ZP, NST, G>(p, ig, 1, lut, lut + kLutBytes);
+  const Rows<S, U> p = {a, a.packed, static_cast<const S*>(a.scales), a.zeros, a.x,
+                        min(a.N, 16 * U) - 1};
+  expert_tiles<W4::kInt4, B, S, ZP, NST, G, U>(p, ig, 1, lut, lut + kLutBytes);
 }
 
-template <int B, typename S, bool ZP, int NST, int G>
+template <int B, typename S, bool ZP, int NST, int G, int U>
 void launch_rows_n(const Int4LinearArgs& a, const Launch& l, hipStream_t stream) {
-  const int lds = kLutBytes + 2 * scale_bytes<ScaleWord<B, S, ZP>>(NST);
-  hipLaunchKernelGGL((int4_rows_kernel<B, S, ZP, NST, G>), dim3(l.grid), dim3(kThreads), lds,
+  const int lds = kLutBytes + 2 * scale_bytes<ScaleWord<B, S, ZP>, U>(NST);
+  hipLaunchKernelGGL((int4_rows_kernel<B, S, ZP, NST, G, U>), dim3(l.grid), dim3(kThreads), lds,
                      stream, a, l.ig);
 }
 
-constexpr int kRowsGroup = 2;
+template <int B, typename S, bool ZP, int U>
+void launch_rows_u(const Int4LinearArgs& a, const Launch& l, hipStream_t stream) {
+  if constexpr (U == 1) {
+    if (l.group > 1) return launch_rows_n<B, S, ZP, 4, kGroup, U>(a, l, stream);
+    if (l.nst > 6) return launch_rows_n<B, S, ZP, 8, 1, U>(a, l, stream);
+  }
+  if (l.nst == 1)
+    launch_rows_n<B, S, ZP, 1, 1, U>(a, l, stream);
+  else if (l.nst == 2)
+    launch_rows_n<B, S, ZP, 2, 1, U>(a, l, stream);
+  else if (l.nst == 3)
+    launch_rows_n<B, S, ZP, 3, 1, U>(a, l, stream);
+  else if (l.nst == 4)
+    launch_rows_n<B, S, ZP, 4, 1, U>(a, l, stream);
+  else
+    launch_rows_n<B, S, ZP, 6, 1, U>(a, l, stream);
+}
 
+// Items of two column tiles share a barrier and its sums; single ones where
+// they spread the columns over the CUs at least a tenth better, and for the
+// longest rows, whose activations leave no registers for two.
 template <int B, typename S, bool ZP>
 void launch_rows(const Int4LinearArgs& a, hipStream_t stream) {
-  const int tiles = (a.N + 31) / 32;
-  Launch l = plan_launch(1, 1, tiles, a.K, kRowsGroup);
-  l.ig.tiles = (tiles + l.group - 1) / l.group * l.group;
-  if (l.group > 1)
-    launch_rows_n<B, S, ZP, 4, kRowsGroup>(a, l, stream);
-  else if (l.nst == 1)
-    launch_rows_n<B, S, ZP, 1, 1>(a, l, stream);
-  else if (l.nst == 2)
-    launch_rows_n<B, S, ZP, 2, 1>(a, l, stream);
-  else if (l.nst == 3)
-    launch_rows_n<B, S, ZP, 3, 1>(a, l, stream);
+  const auto plan = [&](int u) {
+    const int tiles = (a.N + 16 * u - 1) / (16 * u);
+    Launch l = plan_launch(1, 1, tiles, a.K, 8);
+    l.ig.tiles = (tiles + l.group - 1) / l.group * l.group;
+    return l;
+  };
+  const Launch two = plan(2), one = plan(1);
+  if (one.cost * 10 < two.cost * 2 * 9 || one.group > 1 || one.nst > 6)
+    launch_rows_u<B, S, ZP, 1>(a, one, stream);
   else
-    launch_rows_n<B, S, ZP, 4, 1>(a, l, stream);
+    launch_rows_u<B, S, ZP, 2>(a, two, stream);
 }
 
 // More rows: a wavefront holds 16 RT rows x 64 columns of the product, so a

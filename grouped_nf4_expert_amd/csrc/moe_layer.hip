@@ -21,7 +21,6 @@
 namespace gnf4 {
 namespace {
 
-constexpr int kGroup = 2;  // items of a group that shares the activations of a pass
 constexpr int kMaxE = 1024;
 constexpr int kMaxRows = kMoeLayerMaxTokens * 32;  // top_k <= 32
 constexpr int kMaxEntries = kMoeLayerMaxEntries;
@@ -268,7 +267,7 @@ struct GateUp {
     // neighbouring lanes hold an output's gate and up
     for (int i = threadIdx.x & ((64 << log_wk) - 1); i < 512; i += 64 << log_wk) {
       const int o = i >> 1, row = tile_row(o);
-      const float v = team_sum(sums, team, log_wk, i & 1, o);
+      const float v = team_sum<2>(sums, team, log_wk, i & 1, o);
       const float g = __uint_as_float(dpp_u32<0xA0, 0xF>(0u, __float_as_uint(v)));  // even lane's
       const float u = __uint_as_float(dpp_u32<0xF5, 0xF>(0u, __float_as_uint(v)));  // odd lane's
       const int r = en.row0 + min(row, en.cnt - 1);
@@ -299,7 +298,7 @@ struct Down {
     for (int i = threadIdx.x & ((64 << log_wk) - 1); i < 512; i += 64 << log_wk) {
       const int h = i >> 8, o = i & 255, row = tile_row(o);
       const int r = en.row0 + min(row, en.cnt - 1);
-      a.y[(size_t)r * a.H + tile * 32 + h * 16 + tile_col(o)] = team_sum(sums, team, log_wk, h, o);
+      a.y[(size_t)r * a.H + tile * 32 + h * 16 + tile_col(o)] = team_sum<2>(sums, team, log_wk, h, o);
     }
   }
 };
@@ -312,7 +311,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void moe_gate_up_
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   char* slds = lut + kLutBytes;
   Routing L;
-  L.entry = reinterpret_cast<uint32_t*>(slds + 2 * scale_bytes<ScaleWord<B, S, false>>(NST));
+  L.entry = reinterpret_cast<uint32_t*>(slds + 2 * scale_bytes<ScaleWord<B, S, false>, 2>(NST));
   L.row_w = reinterpret_cast<float*>(L.entry + max_entries);
   L.row_tok = reinterpret_cast<uint8_t*>(L.row_w + a.T * a.top_k);
   const int n_entries =
@@ -321,7 +320,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void moe_gate_up_
   lds_barrier();
   const GateUp<S> p = {a, L, a.gu_packed, static_cast<const S*>(a.gu_scales),
                        2 * (size_t)a.I, a.I, a.x};
-  expert_tiles<F, B, S, false, NST, G>(p, ig, n_entries, lut, slds);
+  expert_tiles<F, B, S, false, NST, G, 2>(p, ig, n_entries, lut, slds);
 }
 
 template <W4 F, int B, typename S, int NST, int G>
@@ -330,13 +329,13 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void moe_down_ker
   extern __shared__ __align__(256) char lut[];
   char* slds = lut + kLutBytes;
   uint32_t* entries =
-      reinterpret_cast<uint32_t*>(slds + 2 * scale_bytes<ScaleWord<B, S, false>>(NST));
+      reinterpret_cast<uint32_t*>(slds + 2 * scale_bytes<ScaleWord<B, S, false>, 2>(NST));
   for (int i = threadIdx.x; i <= max_entries; i += kThreads) entries[i] = a.entries[i];
   fill_lut<F>(lut);
   lds_barrier();
   const Down<S> p = {a, entries + 1, a.dn_packed, static_cast<const S*>(a.dn_scales),
                      (size_t)a.H, 16, a.h};
-  expert_tiles<F, B, S, false, NST, G>(p, ig, uniform((int)entries[0]), lut, slds);
+  expert_tiles<F, B, S, false, NST, G, 2>(p, ig, uniform((int)entries[0]), lut, slds);
 }
 
 // out[t] = residual[t] + the fp32 rows of the token's slots, in slot order.
@@ -359,14 +358,14 @@ __global__ __launch_bounds__(kSumThreads) void moe_sum_kernel(MoeLayerArgs a) {
 
 template <W4 F, int B, typename S, int NST, int G>
 void launch_gate_up(const MoeLayerArgs& a, const Launch& l, int max_entries, hipStream_t stream) {
-  const int lds = kLutBytes + 2 * scale_bytes<ScaleWord<B, S, false>>(NST) + 4 * max_entries +
+  const int lds = kLutBytes + 2 * scale_bytes<ScaleWord<B, S, false>, 2>(NST) + 4 * max_entries +
                   5 * a.T * a.top_k;
   hipLaunchKernelGGL((moe_gate_up_kernel<F, B, S, NST, G>), dim3(l.grid), dim3(kThreads), lds,
                      stream, a, l.ig, max_entries);
 }
 template <W4 F, int B, typename S, int NST, int G>
 void launch_down(const MoeLayerArgs& a, const Launch& l, int max_entries, hipStream_t stream) {
-  const int lds = kLutBytes + 2 * scale_bytes<ScaleWord<B, S, false>>(NST) + 4 * (1 + max_entries);
+  const int lds = kLutBytes + 2 * scale_bytes<ScaleWord<B, S, false>, 2>(NST) + 4 * (1 + max_entries);
   hipLaunchKernelGGL((moe_down_kernel<F, B, S, NST, G>), dim3(l.grid), dim3(kThreads), lds,
                      stream, a, l.ig, max_entries);
 }
@@ -382,7 +381,7 @@ void launch_layer(const MoeLayerArgs& a, hipStream_t stream) {
   }
   const int rows = a.T * a.top_k;
   const int experts = a.E < rows ? a.E : rows, max_entries = experts + rows / 16;
-  const Launch gu = plan_launch(experts, max_entries, a.I / 16, a.H, kGroup);
+  const Launch gu = plan_launch(experts, max_entries, a.I / 16, a.H, 4);
   if (gu.group > 1)
     launch_gate_up<F, B, S, 4, kGroup>(a, gu, max_entries, stream);
   else if (gu.nst == 1)
@@ -393,7 +392,7 @@ void launch_layer(const MoeLayerArgs& a, hipStream_t stream) {
     launch_gate_up<F, B, S, 3, 1>(a, gu, max_entries, stream);
   else
     launch_gate_up<F, B, S, 4, 1>(a, gu, max_entries, stream);
-  const Launch dn = plan_launch(experts, max_entries, a.H / 32, a.I, kGroup);
+  const Launch dn = plan_launch(experts, max_entries, a.H / 32, a.I, 4);
   if (dn.group > 1)
     launch_down<F, B, S, 4, kGroup>(a, dn, max_entries, stream);
   else if (dn.nst == 1)

@@ -2,7 +2,7 @@
 // projections share.
 //
 // A work item is an entry -- up to 16 activation rows against one weight
-// matrix, one matrix-core tile -- and 32 weight rows.  The eight wavefronts of
+// matrix, one matrix-core tile -- and U tiles of 16 weight rows.  The eight wavefronts of
 // a workgroup form teams; a team owns an item, its wavefronts split the steps
 // of K between them and their sums meet in LDS.  Workgroups stay resident (one
 // or two per CU) and each team walks a contiguous range of items, so
@@ -21,6 +21,7 @@ namespace gnf4 {
 namespace {
 
 constexpr int kWaves = 8;
+constexpr int kGroup = 2;  // items of a group that shares the activations of a pass
 constexpr int kThreads = kWaves * kWave;
 
 // A value that is the same in every lane, in a scalar register.
@@ -95,20 +96,20 @@ struct RawF32 {
   }
 };
 
-// The scales of a turn in LDS: step s of row r (0..31) of a team, rows side by
+// The scales of an item in LDS: step s of row r (of 16 U) of a team, rows side by
 // side, each step's a word further on so that a fetch's stores (neighbouring
 // lanes hold neighbouring steps) meet different banks.
-template <typename Scale>
+template <typename Scale, int U>
 __device__ __forceinline__ int scale_at(int s, int r) {
-  return s * (32 * (int)sizeof(Scale) + 4 * Scale::kWords) + r * (int)sizeof(Scale);
+  return s * (16 * U * (int)sizeof(Scale) + 4 * Scale::kWords) + r * (int)sizeof(Scale);
 }
-template <typename Scale>
+template <typename Scale, int U>
 __device__ __forceinline__ int team_scales(int nst, int team, int wk) {
-  return team * scale_at<Scale>(nst * wk, 0);
+  return team * scale_at<Scale, U>(nst * wk, 0);
 }
-template <typename Scale>
+template <typename Scale, int U>
 __host__ __device__ constexpr int scale_bytes(int nst) {
-  return kWaves * nst * (32 * (int)sizeof(Scale) + 4 * Scale::kWords);
+  return kWaves * nst * (16 * U * (int)sizeof(Scale) + 4 * Scale::kWords);
 }
 
 // Workgroups per CU: two where a wavefront's activations leave its registers
@@ -123,11 +124,13 @@ constexpr int waves_per_simd(int nst, int g) { return groups_per_cu(nst, g) * kW
 // activations and keep their sums in registers from pass to pass.  Weight
 // addresses are a scalar base that the item and the step move and a lane offset
 // that never moves.
-template <W4 F, int B, typename S, bool ZP, int NST, int G, typename P>
+template <W4 F, int B, typename S, bool ZP, int NST, int G, int U, typename P>
 __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int n_entries,
                                              char* lut, char* slds) {
   typedef ScaleWord<B, S, ZP> Scale;
-  constexpr int kBufs = NST == 3 ? 3 : 4, kAhead = kBufs - 1;
+  // steps held or in flight: 2 KB each with two tiles, 1 KB with one
+  constexpr int kBufs = U == 1 && NST > 2 ? (NST % 3 == 0 ? 6 : 8) : NST == 3 ? 3 : 4;
+  constexpr int kAhead = kBufs - 1;
   constexpr int kUnroll = G > 1 ? G : NST == 1 ? 4 : 2;  // items per turn of the loop
   static_assert(NST * kUnroll % kBufs == 0 && kUnroll % 2 == 0,
                 "the buffers of a step and of an item must be known when compiling");
@@ -152,9 +155,9 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
   int cj = lj, ct = lt;   // and the group whose sums are being formed
   int left = n_mine - 1;  // groups after it
   int lp = 0, lg = 0;
-  uint32_t coff[2];
+  uint32_t coff[U];
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+  for (int u = 0; u < U; ++u)
     coff[u] = (uint32_t)min(u * p.second + col, p.max_row) * (uint32_t)kb + g * 16;
   const uint8_t* cbase;
   const auto weight_row = [&](int j, int tile) {  // of the stack
@@ -179,10 +182,10 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
       }
     }
   };
-  const auto load = [&](u32x4 (&w)[2], int i) {
+  const auto load = [&](u32x4 (&w)[U], int i) {
     const int c = min((lp * wk + kw) * NST + i, steps - 1);
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < U; ++u)
       w[u] = load_codes(cbase, c, coff[u], g, kb);
     if (i == NST - 1) {
       step_on(lj, lt, lp, lg, left);
@@ -192,18 +195,18 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
   // Scales go through LDS: read by each lane from its own row they would cost
   // as many cache lines as the codes.  The team's threads fetch the item's
   // 2 x 16 rows of wk * NST steps in row order, two items ahead.
-  constexpr int kSteps = 32 * NST, kFetch = (kSteps + 63) / 64;  // words per wavefront, per thread
+  constexpr int kSteps = 16 * U * NST, kFetch = (kSteps + 63) / 64;  // words per wavefront, per thread
   int fj = lj, ft = lt, fp = 0, fg = 0, fleft = left;
   uint32_t foff[kFetch];
   int fstep[kFetch], fat[kFetch];
 #pragma unroll
   for (int i = 0; i < kFetch; ++i) {  // row, then step; threads left over repeat the last
-    const int id = min(kw * kWave + lane + i * (wk * kWave), (32 * NST << ig.log_wk) - 1);
+    const int id = min(kw * kWave + lane + i * (wk * kWave), (kSteps << ig.log_wk) - 1);
     const int row = id / NST >> ig.log_wk;
     fstep[i] = id - ((row * NST) << ig.log_wk);
     foff[i] = (uint32_t)min((row & 15) + (row & 16 ? p.second : 0), p.max_row) * (uint32_t)blocks;
     if constexpr (G == 1) foff[i] += scales_first<B>(min(fstep[i], steps - 1), blocks);
-    fat[i] = team_scales<Scale>(NST, team, wk) + scale_at<Scale>(fstep[i], row);
+    fat[i] = team_scales<Scale, U>(NST, team, wk) + scale_at<Scale, U>(fstep[i], row);
   }
   Scale fetched[2][kFetch];
   int fsteps[2] = {0, 0};  // the first step of a fetch
@@ -224,7 +227,7 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
 #pragma unroll
     for (int i = 0; i < kFetch; ++i) {
       align_scales<B, S, ZP>(fetched[buf][i], min(fsteps[buf] + fstep[i], steps - 1), blocks);
-      *reinterpret_cast<Scale*>(slds + buf * scale_bytes<Scale>(NST) + fat[i]) = fetched[buf][i];
+      *reinterpret_cast<Scale*>(slds + buf * scale_bytes<Scale, U>(NST) + fat[i]) = fetched[buf][i];
     }
   };
   // The entry's activations at this wavefront's steps of a pass, each row
@@ -299,7 +302,7 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
   fetch(0);
   set_item();
   __builtin_amdgcn_sched_barrier(0);
-  u32x4 w[kBufs][2];
+  u32x4 w[kBufs][U];
 #pragma unroll
   for (int n = 0; n < kAhead; ++n) load(w[n], n % NST);
   fetch(1);
@@ -308,11 +311,12 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
   put(0);
   lds_barrier();
   // an item's steps of a pass; `it` is its position within a turn of the loop
-  const auto item_steps = [&](int it, f32x4 (&acc)[2]) {
-    acc[0] = acc[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const auto item_steps = [&](int it, f32x4 (&acc)[U]) {
+#pragma unroll
+    for (int h = 0; h < U; ++h) acc[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     fetch(it & 1);
-    const char* mine = slds + (it & 1) * scale_bytes<Scale>(NST) +
-                       team_scales<Scale>(NST, team, wk) + scale_at<Scale>(kw * NST, col);
+    const char* mine = slds + (it & 1) * scale_bytes<Scale, U>(NST) +
+                       team_scales<Scale, U>(NST, team, wk) + scale_at<Scale, U>(kw * NST, col);
 #pragma unroll
     for (int n = 0; n < NST; ++n) {
       const int q = it * NST + n;
@@ -320,8 +324,8 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
       __builtin_amdgcn_sched_barrier(0);  // the loads go first
       // idle steps past the row's end have zero activations
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const Scale sc = *reinterpret_cast<const Scale*>(mine + scale_at<Scale>(n, h * 16));
+      for (int h = 0; h < U; ++h) {
+        const Scale sc = *reinterpret_cast<const Scale*>(mine + scale_at<Scale, U>(n, h * 16));
         acc[h] = step_mac<F, B, S, ZP>(w[q % kBufs][h], sc, x[n], copy, acc[h]);
         // where registers are short, one tile's decode at a time
         if constexpr (G > 1 || F == W4::kMx4 || ZP || groups_per_cu(NST, G) > 1)
@@ -330,21 +334,21 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
     }
     put((it + 1) & 1);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < U; ++h)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if constexpr (F != W4::kInt4) acc[h][r] *= down[r];
   };
   // the wavefronts' sums of an item meet: [wave][tile][register][lane]
   int turn = 0;
-  const auto meet = [&](const f32x4 (&acc)[2], int tile) {
+  const auto meet = [&](const f32x4 (&acc)[U], int tile) {
     char* sums = lut + (turn & 1) * kSumBytes;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < U; ++h)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         *reinterpret_cast<float*>(
-            sums + lds_half(((wave * 2 + h) * 4 + r) * kWave) + lds_half(lane) - 128) = acc[h][r];
+            sums + lds_half(((wave * U + h) * 4 + r) * kWave) + lds_half(lane) - 128) = acc[h][r];
     lds_barrier();
     p.finish(team, ig.log_wk, cj, tile, sums);
     ++turn;
@@ -353,7 +357,7 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
     for (;;) {
 #pragma unroll
       for (int it = 0; it < kUnroll; ++it) {
-        f32x4 acc[2];
+        f32x4 acc[U];
         item_steps(it, acc);
         meet(acc, ct);
         if (turn == rounds) return;
@@ -367,9 +371,11 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
     }
   } else {
     for (int round = 0; round < rounds; ++round) {
-      f32x4 total[G][2];
+      f32x4 total[G][U];
 #pragma unroll
-      for (int it = 0; it < G; ++it) total[it][0] = total[it][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int it = 0; it < G; ++it)
+#pragma unroll
+        for (int h = 0; h < U; ++h) total[it][h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       for (int pass = 0; pass < ig.passes; ++pass) {
         if (round + pass > 0) {
           issue_x(cj, pass);
@@ -377,10 +383,10 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
         }
 #pragma unroll
         for (int it = 0; it < G; ++it) {
-          f32x4 acc[2];
+          f32x4 acc[U];
           item_steps(it, acc);
-          total[it][0] += acc[0];
-          total[it][1] += acc[1];
+#pragma unroll
+          for (int h = 0; h < U; ++h) total[it][h] += acc[h];
           lds_barrier();  // the next scales are in place, the last ones free
         }
       }
@@ -402,51 +408,59 @@ __device__ __forceinline__ int tile_row(int o) { return ((o & 63) >> 4) * 4 + (o
 __device__ __forceinline__ int tile_col(int o) { return o & 15; }
 
 // The sum of a team's wavefronts, in wavefront order.
+template <int U>
 __device__ __forceinline__ float team_sum(const char* sums, int team, int log_wk, int tile, int o) {
-  const char* p = sums + lds_half((((team << log_wk) * 2 + tile) << 8) + o);
-  const auto at = [p](int k) { return *reinterpret_cast<const float*>(p + k * (512 / 32 * 256)); };
+  const char* p = sums + lds_half((((team << log_wk) * U + tile) << 8) + o);
+  const auto at = [p](int k) {
+    return *reinterpret_cast<const float*>(p + k * (U * 256 / 32 * 256));
+  };
   float v = at(0) + at(1);
   if (log_wk > 1) v = v + at(2) + at(3);
   if (log_wk > 2) v = v + at(4) + at(5) + at(6) + at(7);
   return v;
 }
 
-// Wavefronts per team, hence steps per wavefront: the widest team, with the
-// fewest activations to load and hold per wavefront, unless a narrower one
-// takes at least an eighth fewer steps in all when `entries` are routed (a team
-// wider than the row's steps has idle wavefronts).  A wavefront holds the
-// activations of at most four steps; longer rows take passes of four by the
-// whole workgroup.
+// How a projection is launched.  Wavefronts per team, hence steps per
+// wavefront: the widest team, with the fewest activations to load and hold per
+// wavefront, unless a narrower one takes at least an eighth fewer steps in all
+// when there are `entries` (a team wider than the row's steps has idle
+// wavefronts).  A wavefront holds the activations of at most max_nst steps;
+// longer rows take passes of four steps by the whole workgroup.
 struct Launch {
   unsigned grid;
   int nst, group;
   ItemGrid ig;
+  int64_t cost;  // steps that the busiest wavefront takes
 };
-inline Launch plan_launch(int entries, int max_entries, int tiles, int K, int wide_group) {
+inline Launch plan_launch(int entries, int max_entries, int tiles, int K, int max_nst) {
   const int steps = (K + kStep - 1) / kStep;
   const int64_t cus = device_cu_count(), items = (int64_t)entries * tiles;
   int best = 3, nst = (steps + 7) / 8, group = 1, passes = 1;
-  if (nst > 4) {
+  int64_t cost = INT64_MAX;
+  if (nst > max_nst) {
     passes = (nst + 3) / 4;
     nst = 4;
-    group = wide_group;
+    group = kGroup;
+    cost = (items + cus * group - 1) / (cus * group) * group * passes * nst;
   } else {
-    int64_t best_cost = INT64_MAX;
+    int64_t limit = INT64_MAX;
     for (int l = 3; l >= 1; --l) {
       const int n = (steps + (1 << l) - 1) >> l;
       const int64_t teams = cus * groups_per_cu(n, 1) * (kWaves >> l);
-      const int64_t cost = (items + teams - 1) / teams * n * groups_per_cu(n, 1);
-      if (n <= 4 && cost < best_cost) {
+      const int64_t c = (items + teams - 1) / teams * n * groups_per_cu(n, 1);
+      if (n <= max_nst && c < limit) {
         best = l;
         nst = n;
-        best_cost = cost * 7 / 8;
+        cost = c;
+        limit = c * 7 / 8;
       }
     }
   }
   const int teams = kWaves >> best;
   const int64_t need = ((int64_t)max_entries * ((tiles + group - 1) / group) + teams - 1) / teams;
   const int64_t room = cus * groups_per_cu(nst, group);
-  return Launch{(unsigned)(need < room ? need : room), nst, group, ItemGrid{tiles, K, best, passes}};
+  return Launch{(unsigned)(need < room ? need : room), nst, group,
+                ItemGrid{tiles, K, best, passes}, cost};
 }
 
 }  // namespace
