@@ -119,16 +119,16 @@ template <typename S, int U>
 struct Rows {
   typedef RawBf16 Raw;
   static constexpr bool kKeepRaw = true;
-  static constexpr int second = 16, kRows = 16 * U;
+  static constexpr int kRows = 16 * U;
   const Int4LinearArgs& a;
   const uint8_t* codes;
   const S* scales;
   const uint8_t* zeros;
   const uint16_t* x;
-  int max_row;  // the last row of an item that the matrix has
   static constexpr size_t expert_rows = 0;
   __device__ uint32_t entry(int) const { return make_entry(0, 0, a.M); }
   __device__ int row(int r) const { return r; }
+  __device__ int weight_row(int r) const { return min(r, a.N - 1); }
   // the last item ends with the matrix, over rows of the item before it
   __device__ int first_row(int item) const { return min(item * kRows, max(a.N - kRows, 0)); }
   __device__ void finish(int team, int log_wk, int, int item, const char* sums) const {
@@ -149,8 +149,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void int4_rows_ke
   extern __shared__ __align__(256) char lut[];
   fill_lut<W4::kInt4>(lut);
   lds_barrier();
-  const Rows<S, U> p = {a, a.packed, static_cast<const S*>(a.scales), a.zeros, a.x,
-                        min(a.N, 16 * U) - 1};
+  const Rows<S, U> p = {a, a.packed, static_cast<const S*>(a.scales), a.zeros, a.x};
   expert_tiles<W4::kInt4, B, S, ZP, NST, G, U>(p, ig, 1, lut, lut + kLutBytes);
 }
 

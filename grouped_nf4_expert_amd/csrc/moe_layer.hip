@@ -242,42 +242,43 @@ __device__ __forceinline__ float silu(float g) {  // through exp2 and rcp, a few
 // item: the same bits go to the same place, and no store is in a branch, where
 // it would make the compiler wait for loads in flight that it cannot count.
 
-// gate_up: 16 gate rows and their 16 up rows; SwiGLU, scaled by the row's
+// gate_up: 8 U gate rows and their up rows; SwiGLU, scaled by the row's
 // routing weight (so the sums over a token's experts need no further factor)
 // and kept in fp32: one rounding to bf16 would cost as much accuracy as the
 // layer's output rounding.
-template <typename S>
+template <typename S, int U>
 struct GateUp {
   typedef RawBf16 Raw;
   static constexpr bool kKeepRaw = true;
+  static constexpr int kCols = 8 * U;  // outputs per item and token
   const MoeLayerArgs& a;
   const Routing& L;
   const uint8_t* codes;
   const S* scales;
   size_t expert_rows;
-  int second;  // rows from an item's first tile to its second
   const uint16_t* x;
-  static constexpr int max_row = INT_MAX;  // every row of an item exists
   static constexpr const uint8_t* zeros = nullptr;
-  __device__ int first_row(int tile) const { return tile * 16; }
+  __device__ int first_row(int tile) const { return tile * kCols; }
+  __device__ int weight_row(int r) const { return r < kCols ? r : a.I + r - kCols; }
   __device__ uint32_t entry(int j) const { return L.entry[j]; }
   __device__ int row(int r) const { return L.row_tok[r]; }
   __device__ void finish(int team, int log_wk, int j, int tile, const char* sums) const {
     const Entry en = read_entry(L.entry[j]);
     // neighbouring lanes hold an output's gate and up
-    for (int i = threadIdx.x & ((64 << log_wk) - 1); i < 512; i += 64 << log_wk) {
-      const int o = i >> 1, row = tile_row(o);
-      const float v = team_sum<2>(sums, team, log_wk, i & 1, o);
+    for (int i = threadIdx.x & ((64 << log_wk) - 1); i < 256 * U; i += 64 << log_wk) {
+      // two tiles: gates in the first; one: in its first eight columns
+      const int q = i >> 1, o = U == 2 ? q : (q >> 3) * 16 + (i & 1) * 8 + (q & 7);
+      const float v = team_sum<U>(sums, team, log_wk, U == 2 ? i & 1 : 0, o);
       const float g = __uint_as_float(dpp_u32<0xA0, 0xF>(0u, __float_as_uint(v)));  // even lane's
       const float u = __uint_as_float(dpp_u32<0xF5, 0xF>(0u, __float_as_uint(v)));  // odd lane's
-      const int r = en.row0 + min(row, en.cnt - 1);
-      a.h[(uint32_t)(r * a.I + tile * 16 + tile_col(o))] = silu(g) * u * L.row_w[r];
+      const int r = en.row0 + min(tile_row(o), en.cnt - 1);
+      a.h[(uint32_t)(r * a.I + tile * kCols + (q & (kCols - 1)))] = silu(g) * u * L.row_w[r];
     }
   }
 };
 
-// down: 32 weight rows, fp32 sums per grouped row.
-template <typename S>
+// down: 16 U weight rows, fp32 sums per grouped row.
+template <typename S, int U>
 struct Down {
   typedef RawF32 Raw;
   static constexpr bool kKeepRaw = false;  // fp32 values of all steps do not fit; read twice
@@ -286,56 +287,56 @@ struct Down {
   const uint8_t* codes;
   const S* scales;
   size_t expert_rows;
-  int second;
   const float* x;
-  static constexpr int max_row = INT_MAX;
   static constexpr const uint8_t* zeros = nullptr;
-  __device__ int first_row(int tile) const { return tile * 32; }
+  __device__ int first_row(int tile) const { return tile * 16 * U; }
+  __device__ int weight_row(int r) const { return r; }
   __device__ uint32_t entry(int j) const { return entries[j]; }
   __device__ int row(int r) const { return r; }
   __device__ void finish(int team, int log_wk, int j, int tile, const char* sums) const {
     const Entry en = read_entry(entries[j]);
-    for (int i = threadIdx.x & ((64 << log_wk) - 1); i < 512; i += 64 << log_wk) {
-      const int h = i >> 8, o = i & 255, row = tile_row(o);
-      const int r = en.row0 + min(row, en.cnt - 1);
-      a.y[(size_t)r * a.H + tile * 32 + h * 16 + tile_col(o)] = team_sum<2>(sums, team, log_wk, h, o);
+    for (int i = threadIdx.x & ((64 << log_wk) - 1); i < 256 * U; i += 64 << log_wk) {
+      const int h = i >> 8, o = i & 255;
+      const int r = en.row0 + min(tile_row(o), en.cnt - 1);
+      a.y[(size_t)r * a.H + tile * 16 * U + h * 16 + tile_col(o)] =
+          team_sum<U>(sums, team, log_wk, h, o);
     }
   }
 };
 
-template <W4 F, int B, typename S, int NST, int G>
-__global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void moe_gate_up_kernel(MoeLayerArgs a, ItemGrid ig,
-                                                               int max_entries) {
+template <W4 F, int B, typename S, int NST, int U>
+__global__ __launch_bounds__(kThreads, waves_per_simd(NST, 1)) void moe_gate_up_kernel(
+    MoeLayerArgs a, ItemGrid ig, int max_entries) {
   extern __shared__ __align__(256) char lut[];
   static_assert(sizeof(RouteScratch) <= kLutBytes, "the routing's scratch lies in the table");
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   char* slds = lut + kLutBytes;
   Routing L;
-  L.entry = reinterpret_cast<uint32_t*>(slds + 2 * scale_bytes<ScaleWord<B, S, false>, 2>(NST));
+  L.entry = reinterpret_cast<uint32_t*>(slds + 2 * scale_bytes<ScaleWord<B, S, false>, U>(NST));
   L.row_w = reinterpret_cast<float*>(L.entry + max_entries);
   L.row_tok = reinterpret_cast<uint8_t*>(L.row_w + a.T * a.top_k);
   const int n_entries =
       route_all(a, L, *reinterpret_cast<RouteScratch*>(lut), wave, lane, blockIdx.x == 0);
   fill_lut<F>(lut);
   lds_barrier();
-  const GateUp<S> p = {a, L, a.gu_packed, static_cast<const S*>(a.gu_scales),
-                       2 * (size_t)a.I, a.I, a.x};
-  expert_tiles<F, B, S, false, NST, G, 2>(p, ig, n_entries, lut, slds);
+  const GateUp<S, U> p = {a, L, a.gu_packed, static_cast<const S*>(a.gu_scales),
+                          2 * (size_t)a.I, a.x};
+  expert_tiles<F, B, S, false, NST, 1, U>(p, ig, n_entries, lut, slds);
 }
 
-template <W4 F, int B, typename S, int NST, int G>
-__global__ __launch_bounds__(kThreads, waves_per_simd(NST, G)) void moe_down_kernel(MoeLayerArgs a, ItemGrid ig,
-                                                            int max_entries) {
+template <W4 F, int B, typename S, int NST, int U>
+__global__ __launch_bounds__(kThreads, waves_per_simd(NST, 1)) void moe_down_kernel(
+    MoeLayerArgs a, ItemGrid ig, int max_entries) {
   extern __shared__ __align__(256) char lut[];
   char* slds = lut + kLutBytes;
   uint32_t* entries =
-      reinterpret_cast<uint32_t*>(slds + 2 * scale_bytes<ScaleWord<B, S, false>, 2>(NST));
+      reinterpret_cast<uint32_t*>(slds + 2 * scale_bytes<ScaleWord<B, S, false>, U>(NST));
   for (int i = threadIdx.x; i <= max_entries; i += kThreads) entries[i] = a.entries[i];
   fill_lut<F>(lut);
   lds_barrier();
-  const Down<S> p = {a, entries + 1, a.dn_packed, static_cast<const S*>(a.dn_scales),
-                     (size_t)a.H, 16, a.h};
-  expert_tiles<F, B, S, false, NST, G, 2>(p, ig, uniform((int)entries[0]), lut, slds);
+  const Down<S, U> p = {a, entries + 1, a.dn_packed, static_cast<const S*>(a.dn_scales),
+                        (size_t)a.H, a.h};
+  expert_tiles<F, B, S, false, NST, 1, U>(p, ig, uniform((int)entries[0]), lut, slds);
 }
 
 // out[t] = residual[t] + the fp32 rows of the token's slots, in slot order.
@@ -356,18 +357,36 @@ __global__ __launch_bounds__(kSumThreads) void moe_sum_kernel(MoeLayerArgs a) {
   for (int i = 0; i < 4; ++i) a.out[o + i] = f32_to_bf16(v[i]);
 }
 
-template <W4 F, int B, typename S, int NST, int G>
-void launch_gate_up(const MoeLayerArgs& a, const Launch& l, int max_entries, hipStream_t stream) {
-  const int lds = kLutBytes + 2 * scale_bytes<ScaleWord<B, S, false>, 2>(NST) + 4 * max_entries +
-                  5 * a.T * a.top_k;
-  hipLaunchKernelGGL((moe_gate_up_kernel<F, B, S, NST, G>), dim3(l.grid), dim3(kThreads), lds,
-                     stream, a, l.ig, max_entries);
+template <W4 F, int B, typename S, bool kDown, int NST, int U>
+void launch_projection(const MoeLayerArgs& a, const Launch& l, int max_entries, hipStream_t stream) {
+  int lds = kLutBytes + 2 * scale_bytes<ScaleWord<B, S, false>, U>(NST) + 4 * (1 + max_entries);
+  if constexpr (!kDown) lds += 5 * a.T * a.top_k;
+  const auto kernel = kDown ? moe_down_kernel<F, B, S, NST, U> : moe_gate_up_kernel<F, B, S, NST, U>;
+  hipLaunchKernelGGL(kernel, dim3(l.grid), dim3(kThreads), lds, stream, a, l.ig, max_entries);
 }
-template <W4 F, int B, typename S, int NST, int G>
-void launch_down(const MoeLayerArgs& a, const Launch& l, int max_entries, hipStream_t stream) {
-  const int lds = kLutBytes + 2 * scale_bytes<ScaleWord<B, S, false>, 2>(NST) + 4 * (1 + max_entries);
-  hipLaunchKernelGGL((moe_down_kernel<F, B, S, NST, G>), dim3(l.grid), dim3(kThreads), lds,
-                     stream, a, l.ig, max_entries);
+
+// Rows of up to 4096: items of two column tiles, whose sums share a barrier.
+// Longer rows: of one, with up to eight steps of activations per wavefront.
+template <W4 F, int B, typename S, bool kDown>
+void project(const MoeLayerArgs& a, int experts, int max_entries, hipStream_t stream) {
+  const int K = kDown ? a.I : a.H, cols = kDown ? a.H : 2 * a.I;
+  if (K <= 4 * kWaves * kStep) {
+    const Launch l = plan_launch(experts, max_entries, cols / 32, K, 4);
+    if (l.nst == 1)
+      launch_projection<F, B, S, kDown, 1, 2>(a, l, max_entries, stream);
+    else if (l.nst == 2)
+      launch_projection<F, B, S, kDown, 2, 2>(a, l, max_entries, stream);
+    else if (l.nst == 3)
+      launch_projection<F, B, S, kDown, 3, 2>(a, l, max_entries, stream);
+    else
+      launch_projection<F, B, S, kDown, 4, 2>(a, l, max_entries, stream);
+  } else {
+    const Launch l = plan_launch(experts, max_entries, cols / 16, K, 8);
+    if (l.nst <= 6)
+      launch_projection<F, B, S, kDown, 6, 1>(a, l, max_entries, stream);
+    else
+      launch_projection<F, B, S, kDown, 8, 1>(a, l, max_entries, stream);
+  }
 }
 
 template <W4 F, int B, typename S>
@@ -381,28 +400,8 @@ void launch_layer(const MoeLayerArgs& a, hipStream_t stream) {
   }
   const int rows = a.T * a.top_k;
   const int experts = a.E < rows ? a.E : rows, max_entries = experts + rows / 16;
-  const Launch gu = plan_launch(experts, max_entries, a.I / 16, a.H, 4);
-  if (gu.group > 1)
-    launch_gate_up<F, B, S, 4, kGroup>(a, gu, max_entries, stream);
-  else if (gu.nst == 1)
-    launch_gate_up<F, B, S, 1, 1>(a, gu, max_entries, stream);
-  else if (gu.nst == 2)
-    launch_gate_up<F, B, S, 2, 1>(a, gu, max_entries, stream);
-  else if (gu.nst == 3)
-    launch_gate_up<F, B, S, 3, 1>(a, gu, max_entries, stream);
-  else
-    launch_gate_up<F, B, S, 4, 1>(a, gu, max_entries, stream);
-  const Launch dn = plan_launch(experts, max_entries, a.H / 32, a.I, 4);
-  if (dn.group > 1)
-    launch_down<F, B, S, 4, kGroup>(a, dn, max_entries, stream);
-  else if (dn.nst == 1)
-    launch_down<F, B, S, 1, 1>(a, dn, max_entries, stream);
-  else if (dn.nst == 2)
-    launch_down<F, B, S, 2, 1>(a, dn, max_entries, stream);
-  else if (dn.nst == 3)
-    launch_down<F, B, S, 3, 1>(a, dn, max_entries, stream);
-  else
-    launch_down<F, B, S, 4, 1>(a, dn, max_entries, stream);
+  project<F, B, S, false>(a, experts, max_entries, stream);
+  project<F, B, S, true>(a, experts, max_entries, stream);
   hipLaunchKernelGGL(moe_sum_kernel, dim3((a.H / 4 + kSumThreads - 1) / kSumThreads, a.T),
                      dim3(kSumThreads), 0, stream, a);
 }

@@ -158,13 +158,13 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
   uint32_t coff[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    coff[u] = (uint32_t)min(u * p.second + col, p.max_row) * (uint32_t)kb + g * 16;
+    coff[u] = (uint32_t)p.weight_row(u * 16 + col) * (uint32_t)kb + g * 16;
   const uint8_t* cbase;
-  const auto weight_row = [&](int j, int tile) {  // of the stack
+  const auto first_row = [&](int j, int tile) {  // of the stack
     const uint32_t ev = (uint32_t)uniform((int)p.entry(j));
     return (size_t)read_entry(ev).e * p.expert_rows + (size_t)p.first_row(tile);
   };
-  const auto set_item = [&]() { cbase = p.codes + weight_row(lj, lt + lg) * (size_t)kb; };
+  const auto set_item = [&]() { cbase = p.codes + first_row(lj, lt + lg) * (size_t)kb; };
   // one item (of a pass) on; past the last group, the last one again
   const auto step_on = [&](int& j, int& t, int& pass, int& item, int& rest) {
     if constexpr (G > 1) {
@@ -204,14 +204,14 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
     const int id = min(kw * kWave + lane + i * (wk * kWave), (kSteps << ig.log_wk) - 1);
     const int row = id / NST >> ig.log_wk;
     fstep[i] = id - ((row * NST) << ig.log_wk);
-    foff[i] = (uint32_t)min((row & 15) + (row & 16 ? p.second : 0), p.max_row) * (uint32_t)blocks;
+    foff[i] = (uint32_t)p.weight_row(row) * (uint32_t)blocks;
     if constexpr (G == 1) foff[i] += scales_first<B>(min(fstep[i], steps - 1), blocks);
     fat[i] = team_scales<Scale, U>(NST, team, wk) + scale_at<Scale, U>(fstep[i], row);
   }
   Scale fetched[2][kFetch];
   int fsteps[2] = {0, 0};  // the first step of a fetch
   const auto fetch = [&](int buf) {
-    const size_t first = weight_row(fj, ft + fg) * (size_t)blocks;
+    const size_t first = first_row(fj, ft + fg) * (size_t)blocks;
     if constexpr (G > 1) fsteps[buf] = fp * wk * NST;
 #pragma unroll
     for (int i = 0; i < kFetch; ++i) {
@@ -236,20 +236,27 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
   // 4 (l / 16) + r).
   u32x4 x[NST][4];
   f32x4 down;
-  constexpr bool kKeep = P::kKeepRaw || NST == 1;
+  // kept as read until they are scaled, where the registers hold both
+  constexpr bool kKeep = F == W4::kInt4 || (P::kKeepRaw && NST <= 4) || NST == 1;
   typename P::Raw keep[kKeep ? NST : 1][4];
   uint32_t xrow = 0;
   // Register i of a step lies in a block that is in the row or past it as a
   // whole (K is a multiple of the block); past it, the row's start is read and
   // multiplied by zero.
-  const auto inside = [&](int pass, int n, int i) {
-    return ((pass * wk + kw) * NST + n) * kStep + i / (B / 32) * B < K;
+  // The positions are worked out where they are used: as constants of the loop
+  // they would fill the scalar registers.
+  const auto first_k = [&](int pass, int n) {
+    int k = ((pass * wk + kw) * NST + n) * kStep;
+    asm volatile("" : "+s"(k));
+    return k;
   };
+  const auto inside = [&](int k, int i) { return k + i / (B / 32) * B < K; };
   const auto raw = [&](int pass, int n) {
+    const int first = first_k(pass, n);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int k = ((pass * wk + kw) * NST + n) * kStep + (k_of<B>(0, i) - k_of<B>(0, 0));
-      keep[kKeep ? n : 0][i].load(p.x + (inside(pass, n, i) ? k : 0), xrow);
+      const int k = first + (k_of<B>(0, i) - k_of<B>(0, 0));
+      keep[kKeep ? n : 0][i].load(p.x + (inside(first, i) ? k : 0), xrow);
     }
   };
   const auto issue_x = [&](int j, int pass) {
@@ -263,23 +270,26 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
   const auto take_x = [&](int pass) {
     if constexpr (F == W4::kInt4) {  // bf16 as it is
 #pragma unroll
-      for (int n = 0; n < NST; ++n)
+      for (int n = 0; n < NST; ++n) {
+        const int first = first_k(pass, n);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            x[n][i][q] = inside(pass, n, i) ? keep[n][i].v[q] : 0u;
+          for (int q = 0; q < 4; ++q) x[n][i][q] = inside(first, i) ? keep[n][i].v[q] : 0u;
+      }
       return;
     }
     uint32_t top = 0;
 #pragma unroll
     for (int n = 0; n < NST; ++n) {
       if (!kKeep && n > 0) raw(pass, n);
+      const int first = first_k(pass, n);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t m = keep[kKeep ? n : 0][i].max_bits();
-        top = max(top, inside(pass, n, i) ? m : 0u);
+        top = max(top, inside(first, i) ? m : 0u);
       }
+      if constexpr (!kKeep && NST > 4) __builtin_amdgcn_sched_barrier(0);
     }
     top = max(top, (uint32_t)__shfl_xor((int)top, 16, kWave));
     top = max(top, (uint32_t)__shfl_xor((int)top, 32, kWave));
@@ -288,9 +298,10 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
 #pragma unroll
     for (int n = 0; n < NST; ++n) {
       if (!kKeep) raw(pass, n);
+      const int first = first_k(pass, n);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        x[n][i] = keep[kKeep ? n : 0][i].half(inside(pass, n, i) ? up : 0.0f);
+        x[n][i] = keep[kKeep ? n : 0][i].half(inside(first, i) ? up : 0.0f);
       if constexpr (!kKeep) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
@@ -424,13 +435,17 @@ __device__ __forceinline__ float team_sum(const char* sums, int team, int log_wk
 // wavefront: the widest team, with the fewest activations to load and hold per
 // wavefront, unless a narrower one takes at least an eighth fewer steps in all
 // when there are `entries` (a team wider than the row's steps has idle
-// wavefronts).  A wavefront holds the activations of at most max_nst steps;
-// longer rows take passes of four steps by the whole workgroup.
+// wavefronts).  Two steps per wavefront, two workgroups per CU, count a quarter
+// more: they stream slower than four steps of one workgroup (64 experts' 4096 x
+// 2048 matrices 49 against 43 us, 100 experts' 7168 x 2048 ones 243 against
+// 217 us); one step of two workgroups does not (29 against 35 us with two steps
+// over rows of 1024).  A wavefront holds the activations of at most max_nst
+// steps; longer rows take passes of four steps by the whole workgroup.
 struct Launch {
   unsigned grid;
   int nst, group;
   ItemGrid ig;
-  int64_t cost;  // steps that the busiest wavefront takes
+  int64_t cost;  // of the busiest CU's wavefronts, in quarter steps
 };
 inline Launch plan_launch(int entries, int max_entries, int tiles, int K, int max_nst) {
   const int steps = (K + kStep - 1) / kStep;
@@ -441,13 +456,14 @@ inline Launch plan_launch(int entries, int max_entries, int tiles, int K, int ma
     passes = (nst + 3) / 4;
     nst = 4;
     group = kGroup;
-    cost = (items + cus * group - 1) / (cus * group) * group * passes * nst;
+    cost = (items + cus * group - 1) / (cus * group) * group * passes * nst * 4;
   } else {
     int64_t limit = INT64_MAX;
     for (int l = 3; l >= 1; --l) {
       const int n = (steps + (1 << l) - 1) >> l;
-      const int64_t teams = cus * groups_per_cu(n, 1) * (kWaves >> l);
-      const int64_t c = (items + teams - 1) / teams * n * groups_per_cu(n, 1);
+      const int64_t one = cus * (kWaves >> l), all = one * groups_per_cu(n, 1);
+      const int64_t rounds = (items + all - 1) / all;
+      const int64_t c = rounds * n * (items > one ? groups_per_cu(n, 1) * (n == 2 ? 5 : 4) : 4);
       if (n <= max_nst && c < limit) {
         best = l;
         nst = n;
