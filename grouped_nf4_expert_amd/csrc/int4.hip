@@ -31,10 +31,25 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   }
 }
 
-// Eight weights per thread, G / 8 neighbouring lanes per group.  The code of
-// w is the number of midpoints (j + 1/2 - z) s below w: the nearest level,
-// ties to the lower code.  The products are exact in fp64 (a scale has 24
-// bits, a midpoint 5), so the comparison is exact.
+// The code of w: the number of midpoints (m + 1/2 - z) s below it, m = 0..14,
+// which is the nearest level, ties to the lower code.  An approximate quotient
+// finds it to within one (its error is far below half a step), and the two
+// midpoints beside the guess settle it: their products are exact in fp64 (a
+// scale has 24 bits, a midpoint 5), so the comparisons are.  A NaN lies above
+// nothing; among infinite midpoints every value but -inf is above the negative
+// ones.
+__device__ __forceinline__ int int4_code(float w, double s, double inv_s, int z) {
+  const double x = (double)w, zz = (double)z;
+  const double q = ceil(x * inv_s + zz - 0.5);
+  const double c = fmin(fmax(q, 0.0), 15.0);
+  int n = (int)c;
+  n += n < 15 && x > (c + 0.5 - zz) * s ? 1 : 0;
+  n -= n > 0 && n == (int)c && !(x > (c - 0.5 - zz) * s) ? 1 : 0;
+  if (s == INFINITY) n = x > -INFINITY ? z : 0;
+  return s == 0.0 ? z : n;
+}
+
+// Eight weights per thread, G / 8 neighbouring lanes per group.
 template <typename WT, typename S, int G, bool ZP>
 __global__ __launch_bounds__(kPackThreads) void int4_pack_kernel(const WT* __restrict__ w,
                                                                  int64_t n8,
@@ -56,29 +71,15 @@ __global__ __launch_bounds__(kPackThreads) void int4_pack_kernel(const WT* __res
       hi = fmaxf(hi, __shfl_xor(hi, o, kWave));
       if constexpr (ZP) lo = fmaxf(lo, __shfl_xor(lo, o, kWave));
     }
-    // fp32 quotients, correctly rounded (an fp64 quotient rounded again is)
-    const float s32 = ZP ? (float)((double)hi / 15.0) + (float)((double)lo / 15.0)
-                         : (float)((double)hi / 7.0);
+    const float s32 = ZP ? hi / 15.0f + lo / 15.0f : hi / 7.0f;
     const S stored = round_scale(s32, S{});
-    const double s = (double)scale_f32(stored);
-    int z = 8;
-    if constexpr (ZP) {
-      z = 0;
-#pragma unroll
-      for (int j = 0; j < 15; ++j) z += (double)lo > (j + 0.5) * s ? 1 : 0;
-      if (s == 0.0) z = 0;
-    }
+    const double s = (double)scale_f32(stored), inv_s = __builtin_amdgcn_rcp(s);
+    const int z = ZP ? int4_code(lo, s, inv_s, 0) : 8;
     uint32_t word = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const double x = (double)v[j];
-      int c = 0;
-#pragma unroll
-      for (int m = 0; m < 15; ++m) c += x > (m + 0.5 - (double)z) * s ? 1 : 0;
-      if (s == 0.0) c = z;
+    for (int j = 0; j < 8; ++j)
       // byte j / 2, the first of the two in the high nibble
-      word |= (uint32_t)c << ((j >> 1) * 8 + ((j & 1) ? 0 : 4));
-    }
+      word |= (uint32_t)int4_code(v[j], s, inv_s, z) << ((j >> 1) * 8 + ((j & 1) ? 0 : 4));
     reinterpret_cast<uint32_t*>(packed)[i] = word;
     if (i % (G / 8) == 0) {
       scales[i / (G / 8)] = stored;
