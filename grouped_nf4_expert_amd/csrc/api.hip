@@ -145,6 +145,7 @@ static bool valid_int4_group(int32_t group, int64_t K) {
 }
 // rows of one int4 linear call: 64 per workgroup along the grid's y
 constexpr int64_t kInt4MaxRows = (int64_t)1 << 20;
+constexpr int64_t kInt4MaxK = (int64_t)1 << 27;  // 32-bit offsets over 32 rows
 
 // What gnf4_moe_layer serves: the route/sort's limits, up to
 // kMoeLayerMaxTokens tokens.
@@ -801,7 +802,7 @@ gnf4_status gnf4_int4_linear(const uint16_t* x, int64_t M, const uint8_t* packed
   if (!valid_int4_group(group, K) || N <= 0 || M < 0) return GNF4_ERR_INVALID_ARG;
   if (!valid_dtype(scale_dtype)) return GNF4_ERR_INVALID_ARG;
   if (M == 0) return GNF4_OK;
-  if (M > kInt4MaxRows || N >= ((int64_t)1 << 30) || K >= ((int64_t)1 << 30))
+  if (M > kInt4MaxRows || N >= ((int64_t)1 << 30) || K > kInt4MaxK)
     return GNF4_ERR_UNSUPPORTED;
   if (!x || !packed || !scales || !y) return GNF4_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(packed, 16) || !aligned(scales, dtype_bytes(scale_dtype)) ||

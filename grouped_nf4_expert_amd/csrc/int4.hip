@@ -197,15 +197,16 @@ void launch_rows(const Int4LinearArgs& a, hipStream_t stream) {
     launch_rows_u<B, S, ZP, 2>(a, two, stream);
 }
 
-// More rows: a wavefront holds 16 RT rows x 64 columns of the product, so a
-// decoded operand serves RT products and an activation fragment four, and the
+// More rows, few tiles: a wavefront holds 32 rows x 64 columns of the product, so
+// a decoded operand serves two products and an activation fragment four, and the
 // eight wavefronts of a workgroup split the steps of K; their sums meet in LDS,
-// in wavefront order.
+// in wavefront order.  K is a step or more.
 constexpr int kGemmCols = 4;  // column tiles of 16
 
-template <int B, typename S, bool ZP, int RT>
+template <int B, typename S, bool ZP>
 __global__ __launch_bounds__(kThreads) void int4_gemm_kernel(Int4LinearArgs a) {
   typedef ScaleWord<B, S, ZP> Scale;
+  constexpr int RT = 2;
   extern __shared__ __align__(256) char lut[];
   fill_lut<W4::kInt4>(lut);
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
@@ -230,9 +231,9 @@ __global__ __launch_bounds__(kThreads) void int4_gemm_kernel(Int4LinearArgs a) {
 #pragma unroll
     for (int t = 0; t < kGemmCols; ++t) {
       d[t] = load_codes(a.packed + wrow[t] * kb, c, (uint32_t)(g * 16), g, kb);
-      load_scales<B, S, ZP, true>(static_cast<const S*>(a.scales) + wrow[t] * blocks,
-                                  ZP ? a.zeros + wrow[t] * blocks : nullptr,
-                                  (uint32_t)scales_first<B>(c, blocks), blocks, s[t]);
+      load_scales<B, S, ZP, false>(static_cast<const S*>(a.scales) + wrow[t] * blocks,
+                                   ZP ? a.zeros + wrow[t] * blocks : nullptr,
+                                   (uint32_t)scales_first<B>(c, blocks), blocks, s[t]);
     }
   };
   load(min(wave, steps - 1), wn, scn);
@@ -325,21 +326,232 @@ __global__ __launch_bounds__(kThreads) void int4_gemm_kernel(Int4LinearArgs a) {
   }
 }
 
-template <int B, typename S, bool ZP, int RT>
-void launch_gemm(const Int4LinearArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((int4_gemm_kernel<B, S, ZP, RT>),
-                     dim3((a.N + 63) / 64, (a.M + 16 * RT - 1) / (16 * RT)), dim3(kThreads),
-                     kLutBytes, stream, a);
+// Enough rows and columns to fill the chip: a workgroup makes 16 RT rows x 128
+// columns, a wavefront 16 RT x 32 over every other step of K (so two wavefronts
+// share a SIMD).  The activations of a turn, two steps, lie in LDS, with their
+// sums over each scale block where there are zero points; the weights of the
+// turn after the next are in flight meanwhile.  Workgroups stay resident and walk
+// the tiles.  SHORT: K is less than a step.
+constexpr int kTileCols = 128;
+constexpr int kTileRow = kStep * 2 + 16;  // bytes of a row's step: 16 lanes meet 16 banks sets
+
+template <int B, typename S, bool ZP, int RT, bool SHORT>
+__global__ __launch_bounds__(kThreads, kWaves / 4) void int4_tile_kernel(Int4LinearArgs a) {
+  typedef ScaleWord<B, S, ZP> Scale;
+  constexpr int kRows = 16 * RT, kBlocks = kStep / B, kPer = B / 32;
+  constexpr int kXBytes = 2 * kRows * kTileRow;  // of a turn
+  constexpr int kPerRow = kThreads / kRows;      // threads that stage a row
+  constexpr int kPieces = 2 * kStep / 8 / kPerRow;  // 16-byte pieces of each
+  extern __shared__ __align__(256) char lut[];
+  char* xs = lut + kLutBytes;
+  float* zs = reinterpret_cast<float*>(xs + 2 * kXBytes);  // [turn & 1][step][block][row]
+  fill_lut<W4::kInt4>(lut);
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const int g = lane >> 4, col = lane & 15;
+  const int half = wave >> 2, nw = wave & 3;
+  const int kb = a.K / 2, blocks = a.K / B, steps = (a.K + kStep - 1) / kStep;
+  const int turns = (steps + 1) / 2;
+  const uint32_t copy = lut_copy(lane);
+  const int srow = threadIdx.x / kPerRow, spiece = threadIdx.x % kPerRow;
+  const int mt = (a.M + kRows - 1) / kRows, nt = (a.N + kTileCols - 1) / kTileCols;
+  // neighbouring workgroups go to different XCDs: the row tiles of a column
+  // tile follow each other on one of them, and its L2 has the weights
+  const int64_t total = (int64_t)((nt + 7) / 8 * 8) * mt;
+  for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
+    const int64_t q8 = id >> 3;
+    const int64_t ct = q8 / mt * 8 + (id & 7);
+    if (ct >= nt) continue;
+    const int n0 = (int)ct * kTileCols + nw * 32, m0 = (int)(q8 % mt) * kRows;
+    const uint8_t* codes[2];
+    const S* scales[2];
+    const uint8_t* zeros[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const size_t n = min(n0 + t * 16 + col, a.N - 1);
+      codes[t] = a.packed + n * kb;
+      scales[t] = static_cast<const S*>(a.scales) + n * blocks;
+      zeros[t] = ZP ? a.zeros + n * blocks : nullptr;
+    }
+    const uint16_t* xrow = a.x + (size_t)min(m0 + srow, a.M - 1) * a.K;
+    const auto load_w = [&](int turn, u32x4 (&w)[2], Scale (&sc)[2]) {
+      const int c = min(2 * turn + half, steps - 1);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        w[t] = load_codes(codes[t], c, (uint32_t)(g * 16), g, kb);
+        load_scales<B, S, ZP, SHORT>(scales[t], zeros[t], (uint32_t)scales_first<B>(c, blocks),
+                                     blocks, sc[t]);
+      }
+    };
+    u32x4 xr[kPieces];
+    const auto load_x = [&](int turn) {
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int k = turn * 2 * kStep + (spiece + j * kPerRow) * 8;
+        xr[j] = *reinterpret_cast<const u32x4*>(xrow + (k < a.K ? k : 0));
+      }
+    };
+    const auto store_x = [&](int turn) {
+      char* to = xs + (turn & 1) * kXBytes;
+      float sum[kPieces];
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int p = spiece + j * kPerRow;
+        if (turn * 2 * kStep + p * 8 >= a.K) xr[j] = u32x4{0u, 0u, 0u, 0u};
+        *reinterpret_cast<u32x4*>(to + ((p >> 4) * kRows + srow) * kTileRow + (p & 15) * 16) = xr[j];
+        if constexpr (ZP) {
+          sum[j] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sum[j] += __uint_as_float(xr[j][i] << 16) + __uint_as_float(xr[j][i] & 0xffff0000u);
+        }
+      }
+      if constexpr (ZP) {
+        constexpr int kOwn = B / 8 > kPerRow ? B / 8 / kPerRow : 1;  // a block's pieces per thread
+        constexpr int kLanes = B / 8 / kOwn;
+#pragma unroll
+        for (int j = 0; j < kPieces; j += kOwn) {
+#pragma unroll
+          for (int i = 1; i < kOwn; ++i) sum[j] += sum[j + i];
+#pragma unroll
+          for (int o = 1; o < kLanes; o *= 2) {  // the mirrors swap equal halves
+            const uint32_t v = __float_as_uint(sum[j]);
+            sum[j] += __uint_as_float(o == 1   ? dpp_u32<0xB1, 0xF>(0u, v)
+                                      : o == 2 ? dpp_u32<0x4E, 0xF>(0u, v)
+                                      : o == 4 ? dpp_u32<0x141, 0xF>(0u, v)
+                                               : dpp_u32<0x140, 0xF>(0u, v));
+          }
+          const int p = spiece + j * kPerRow;
+          if (spiece % kLanes == 0)
+            zs[((turn & 1) * 2 * kBlocks + p / (B / 8)) * kRows + srow] = sum[j];
+        }
+      }
+    };
+    f32x4 acc[2][RT];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[t][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 w[2][2];
+    Scale sc[2][2];
+    load_x(0);
+    load_w(0, w[0], sc[0]);
+    load_w(1, w[1], sc[1]);
+    lds_barrier();  // the sums of the tile before are read
+    store_x(0);
+    load_x(1);
+    lds_barrier();
+    const auto body = [&](int turn, u32x4 (&wt)[2], Scale (&st)[2]) {
+      u32x4 d[2];
+      Scale s[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        d[t] = wt[t];
+        s[t] = st[t];
+        arrange<B>(d[t]);
+        align_scales<B, S, ZP>(s[t], min(2 * turn + half, steps - 1), blocks);
+      }
+      load_w(turn + 2, wt, st);
+      const char* from = xs + (turn & 1) * kXBytes + (half * kRows + col) * kTileRow;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        f32x4 p[2][RT];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < RT; ++r) p[t][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int i = b * kPer + j;
+          u32x4 x[RT];
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            x[r] = *reinterpret_cast<const u32x4*>(from + r * 16 * kTileRow + k_of<B>(g, i) * 2);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const u32x4 e = decode8<W4::kInt4>(d[t][i], copy);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) p[t][r] = mfma16<W4::kInt4>(x[r], e, p[t][r]);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          f32x4 sum;
+          if constexpr (ZP)
+            sum = *reinterpret_cast<const f32x4*>(
+                zs + (((turn & 1) * 2 + half) * kBlocks + b) * kRows + r * 16 + g * 4);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if constexpr (ZP) p[t][r][q] = fmaf((float)(8 - s[t].zero(b)), sum[q], p[t][r][q]);
+              acc[t][r][q] = fmaf(s[t].at(b), p[t][r][q], acc[t][r][q]);
+            }
+        }
+        if constexpr (ZP) __builtin_amdgcn_sched_barrier(0);  // registers: one block at a time
+      }
+      store_x(turn + 1);
+      load_x(turn + 2);
+      lds_barrier();
+    };
+    for (int turn = 0; turn < turns; turn += 2) {
+      body(turn, w[0], sc[0]);
+      if (turn + 1 < turns) body(turn + 1, w[1], sc[1]);
+    }
+    // the halves exchange a column tile each, where the activations were
+    float* red = reinterpret_cast<float*>(xs) + lane;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        red[(((1 - half) * 4 + nw) * RT * 4 + r * 4 + q) * kWave] = half ? acc[0][r][q] : acc[1][r][q];
+    lds_barrier();
+    const int n = n0 + half * 16 + col;
+    const float bias = a.bias ? bf16_to_f32(a.bias[min(n, a.N - 1)]) : 0.0f;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int m = m0 + r * 16 + g * 4 + q;
+        const float y = (half ? acc[1][r][q] : acc[0][r][q]) +
+                        red[((half * 4 + nw) * RT * 4 + r * 4 + q) * kWave];
+        if (m < a.M && n < a.N) a.y[(size_t)m * a.N + n] = f32_to_bf16(y + bias);
+      }
+  }
+}
+
+template <int B, typename S, bool ZP, int RT, bool SHORT>
+void launch_tile(const Int4LinearArgs& a, hipStream_t stream) {
+  const int lds = kLutBytes + 2 * (2 * 16 * RT * kTileRow) +
+                  (ZP ? 2 * 2 * (kStep / B) * 16 * RT * 4 : 0);
+  const int64_t mt = (a.M + 16 * RT - 1) / (16 * RT);
+  const int64_t nt = ((int64_t)a.N + kTileCols - 1) / kTileCols;
+  const int64_t total = (nt + 7) / 8 * 8 * mt, cus = (device_cu_count() + 7) / 8 * 8;
+  hipLaunchKernelGGL((int4_tile_kernel<B, S, ZP, RT, SHORT>), dim3((unsigned)(total < cus ? total : cus)),
+                     dim3(kThreads), lds, stream, a);
 }
 
 template <int B, typename S, bool ZP>
+void launch_gemm(const Int4LinearArgs& a, unsigned mt, unsigned nt, hipStream_t stream) {
+  hipLaunchKernelGGL((int4_gemm_kernel<B, S, ZP>), dim3(nt, mt), dim3(kThreads), kLutBytes,
+                     stream, a);
+}
+
+// Tiles of 32 x 64 with K split over the workgroup while there are no more of
+// them than CUs (64 x 7168 x 2048 14 us against 23 with the larger tiles, 128 x
+// 4096 x 7168 31 against 57); beyond that the larger tiles (256 x 7168 x 2048 22
+// us against 51, 1024 x 2880 x 2880 55 against 89).  Blocks of 32 with zero points
+// have the registers for 32 rows only.
+template <int B, typename S, bool ZP>
 void launch_linear_rt(const Int4LinearArgs& a, hipStream_t stream) {
-  if (a.M <= 16)
-    launch_rows<B, S, ZP>(a, stream);
-  else if (a.M <= 32)
-    launch_gemm<B, S, ZP, 2>(a, stream);
-  else
-    launch_gemm<B, S, ZP, 4>(a, stream);
+  if (a.M <= 16) return launch_rows<B, S, ZP>(a, stream);
+  const int64_t mt = (a.M + 31) / 32, nt = ((int64_t)a.N + 63) / 64;
+  if (B < kStep && a.K < kStep) {
+    if constexpr (B < kStep) launch_tile<B, S, ZP, 2, true>(a, stream);
+  } else if (mt * nt <= device_cu_count()) {
+    launch_gemm<B, S, ZP>(a, (unsigned)mt, (unsigned)nt, stream);
+  } else {
+    launch_tile<B, S, ZP, B == 32 && ZP ? 2 : 4, false>(a, stream);
+  }
 }
 
 template <int B, typename S>

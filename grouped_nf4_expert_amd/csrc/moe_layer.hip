@@ -331,8 +331,11 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(NST, 1)) void moe_down_ker
   char* slds = lut + kLutBytes;
   uint32_t* entries =
       reinterpret_cast<uint32_t*>(slds + 2 * scale_bytes<ScaleWord<B, S, false>, U>(NST));
-  for (int i = threadIdx.x; i <= max_entries; i += kThreads) entries[i] = a.entries[i];
+  // the first of the list travels while the table is made
+  const uint32_t own = a.entries[min((int)threadIdx.x, max_entries)];
   fill_lut<F>(lut);
+  if ((int)threadIdx.x <= max_entries) entries[threadIdx.x] = own;
+  for (int i = threadIdx.x + kThreads; i <= max_entries; i += kThreads) entries[i] = a.entries[i];
   lds_barrier();
   const Down<S, U> p = {a, entries + 1, a.dn_packed, static_cast<const S*>(a.dn_scales),
                         (size_t)a.H, a.h};
@@ -340,7 +343,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(NST, 1)) void moe_down_ker
 }
 
 // out[t] = residual[t] + the fp32 rows of the token's slots, in slot order.
-constexpr int kSumThreads = 256;
+constexpr int kSumThreads = 64, kSumSlots = 8;
 
 __global__ __launch_bounds__(kSumThreads) void moe_sum_kernel(MoeLayerArgs a) {
   const int q = blockIdx.x * kSumThreads + threadIdx.x;  // four columns each
@@ -351,8 +354,19 @@ __global__ __launch_bounds__(kSumThreads) void moe_sum_kernel(MoeLayerArgs a) {
   if (a.residual)
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = bf16_to_f32(a.residual[o + i]);
-  for (int j = 0; j < a.top_k; ++j)
-    v += *reinterpret_cast<const f32x4*>(a.y + (size_t)a.slot_rows[t * a.top_k + j] * a.H + q * 4);
+  for (int j0 = 0; j0 < a.top_k; j0 += kSumSlots) {  // requested together, added in slot order
+    int row[kSumSlots];
+#pragma unroll
+    for (int j = 0; j < kSumSlots; ++j)
+      row[j] = a.slot_rows[t * a.top_k + min(j0 + j, a.top_k - 1)];
+    f32x4 y[kSumSlots];
+#pragma unroll
+    for (int j = 0; j < kSumSlots; ++j)
+      y[j] = *reinterpret_cast<const f32x4*>(a.y + (size_t)row[j] * a.H + q * 4);
+#pragma unroll
+    for (int j = 0; j < kSumSlots; ++j)
+      if (j0 + j < a.top_k) v += y[j];
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) a.out[o + i] = f32_to_bf16(v[i]);
 }

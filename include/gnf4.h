@@ -364,9 +364,9 @@ gnf4_status gnf4_int4_pack(const void* w, int32_t w_dtype, int64_t N, int64_t K,
  *
  * Products of activations and codes are exact; a group's sum and the sums over
  * groups are fp32, y is rounded once.  Any M (one row up to a prompt's chunk)
- * and any N; the weights are read once per 64 rows.  Deterministic; a row's
- * result does not depend on the other rows.
- * Limits: M <= 2^20, N and K below 2^30.  Errors: GNF4_ERR_INVALID_ARG,
+ * and any N; the weights are read once up to 16 rows, then once per 32 or 64.
+ * Deterministic; what the other rows hold does not change a row's result.
+ * Limits: M <= 2^20, N below 2^30, K <= 2^27.  Errors: GNF4_ERR_INVALID_ARG,
  * GNF4_ERR_UNSUPPORTED, GNF4_ERR_NOT_DEVICE_PTR, GNF4_ERR_HIP.
  */
 gnf4_status gnf4_int4_linear(const uint16_t* x, int64_t M, const uint8_t* packed,

@@ -86,6 +86,31 @@ def test_pack_bits(group, zero_points, w_dtype, scale):
             assert np.array_equal(zeros.cpu().numpy(), z)
 
 
+@pytest.mark.parametrize("zero_points", [False, True])
+@pytest.mark.parametrize("scale", ["f32", "bf16"])
+def test_pack_bits_beside_the_midpoints(zero_points, scale):
+    """Weights one fp32 step to either side of every midpoint, over scales from
+    subnormal to the largest."""
+    rng = np.random.default_rng(31)
+    with np.errstate(over="ignore", under="ignore"):
+        s = np.float32(2.0) ** rng.integers(-149, 124, (400, 1)).astype(np.float32)
+        s = (s * rng.uniform(1, 2, (400, 1))).astype(np.float32)
+        mid = (rng.integers(-7, 7, (400, 32)) + 0.5).astype(np.float32) * s
+        w = np.stack([mid, np.nextafter(mid, np.float32(np.inf)),
+                      np.nextafter(mid, np.float32(-np.inf)), -mid], 2).reshape(400, 128)
+        w[:, 0] = 7.0 * s[:, 0]
+    w = np.where(np.isfinite(w), w, np.float32(3e38)).astype(np.float32)
+    for group in (32, 128):
+        packed, scales, zeros = gnf4.int4_pack(torch.from_numpy(w).to(DEV), group, zero_points,
+                                               SCALES[scale])
+        torch.cuda.synchronize()
+        p, sc, z = oracle.ref_int4_pack(w, group, zero_points, scale)
+        assert np.array_equal(scales.float().cpu().numpy().view(np.uint32), sc.view(np.uint32))
+        assert np.array_equal(packed.cpu().numpy(), p)
+        if z is not None:
+            assert np.array_equal(zeros.cpu().numpy(), z)
+
+
 def test_pack_stack_is_rows_and_empty_like_shapes():
     w = bf16_dev(_pack_input(12, 256, 64, 3)).view(3, 4, 256)
     packed, scales, zeros = gnf4.int4_pack(w, 64, True)
@@ -119,6 +144,29 @@ def test_linear_parity(M, N, K, group, zero_points, scale):
     again = gnf4.int4_linear(x, packed, scales, zeros, bias)
     torch.cuda.synchronize()
     assert torch.equal(again, guard[1:M + 1])
+
+
+@pytest.mark.parametrize("M,N,K,group", [
+    (130, 3400, 160, 32), (300, 1700, 320, 64), (1030, 600, 192, 32), (257, 2500, 384, 128),
+    (97, 6000, 1152, 128), (520, 1100, 2880, 32), (33, 70, 32, 32), (70, 300, 96, 32),
+    (50, 33, 64, 64), (2000, 515, 64, 32), (600, 1030, 128, 128)])
+@pytest.mark.parametrize("zero_points", [False, True])
+@pytest.mark.parametrize("scale", ["f32", "bf16"])
+def test_linear_many_tiles(M, N, K, group, zero_points, scale):
+    """More tiles than the chip has CUs, and rows shorter than a step."""
+    test_linear_parity(M, N, K, group, zero_points, scale)
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 5, 8, 9, 12, 16, 17, 23, 24, 31, 32, 33, 40, 47, 48,
+                                   56, 64, 65, 100])
+@pytest.mark.parametrize("N", [13, 600, 4500])
+def test_linear_row_lengths(steps, N):
+    """Every split of a row over the wavefronts, with a row that ends inside
+    its last step where the group allows."""
+    for group in (32, 64, 128):
+        zp = (steps + group // 32) % 2 == 0
+        K = steps * 128 - (group if group < 128 else 0)
+        test_linear_parity(1 + steps % 16, N, K, group, zp, "bf16" if steps % 2 else "f32")
 
 
 def test_linear_rows_do_not_depend_on_each_other():
@@ -188,6 +236,23 @@ def test_linear_on_another_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, refs[i])
+
+
+def test_linear_on_two_streams_at_once():
+    rng = np.random.default_rng(14)
+    packed, scales, zeros = _weights(rng, 700, 1024, 32, True, "f32")
+    xs = [bf16_dev(rng.standard_normal((m, 1024))) for m in (1, 40, 500)]
+    refs = [gnf4.int4_linear(x, packed, scales, zeros) for x in xs]
+    outs = [torch.empty_like(r) for r in refs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, o, s in zip(xs, outs, streams):
+            with torch.cuda.stream(s):
+                gnf4.int4_linear(x, packed, scales, zeros, out=o)
+    torch.cuda.synchronize()
+    for o, r in zip(outs, refs):
+        assert torch.equal(o, r)
 
 
 # ---------------------------------------------------------------- refusals
