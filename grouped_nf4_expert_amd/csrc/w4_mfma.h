@@ -280,10 +280,11 @@ __device__ __forceinline__ void align_scales(ScaleWord<B, S, ZP>& w, int c, int 
 
 // The 16 bytes of step c of the rows at codes + coff (coff includes the lane
 // group's 16 bytes).  A row has kb bytes; past its end a lane reads the step's
-// first bytes again (the activations there are zero).
+// first bytes again (the activations there are zero).  Where `mask` is zero all
+// lanes read the step's first bytes of the first row.
 __device__ __forceinline__ u32x4 load_codes(const uint8_t* codes, int c, uint32_t coff, int g,
-                                            int kb) {
-  const uint32_t co = c * (kStep / 2) + g * 16 < kb ? coff : coff - (uint32_t)(g * 16);
+                                            int kb, uint32_t mask = ~0u) {
+  const uint32_t co = (c * (kStep / 2) + g * 16 < kb ? coff : coff - (uint32_t)(g * 16)) & mask;
   return __builtin_nontemporal_load(
       reinterpret_cast<const u32x4*>(codes + c * (kStep / 2) + co));
 }

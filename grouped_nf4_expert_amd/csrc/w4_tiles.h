@@ -165,8 +165,9 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
     return (size_t)read_entry(ev).e * p.expert_rows + (size_t)p.first_row(tile);
   };
   const auto set_item = [&]() { cbase = p.codes + first_row(lj, lt + lg) * (size_t)kb; };
-  // one item (of a pass) on; past the last group, the last one again
-  const auto step_on = [&](int& j, int& t, int& pass, int& item, int& rest) {
+  // one item (of a pass) on; past the last group the last one again, where a
+  // zero mask leaves one line to read (whole tiles cost two of ten rounds)
+  const auto step_on = [&](int& j, int& t, int& pass, int& item, int& rest, uint32_t& mask) {
     if constexpr (G > 1) {
       if (++item < G) return;
       item = 0;
@@ -180,15 +181,18 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
         t = 0;
         j = uniform(j + 1);
       }
+    } else {
+      mask = 0u;
     }
   };
+  uint32_t lmask = ~0u, fmask = ~0u;
   const auto load = [&](u32x4 (&w)[U], int i) {
     const int c = min((lp * wk + kw) * NST + i, steps - 1);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      w[u] = load_codes(cbase, c, coff[u], g, kb);
+      w[u] = load_codes(cbase, c, coff[u], g, kb, lmask);
     if (i == NST - 1) {
-      step_on(lj, lt, lp, lg, left);
+      step_on(lj, lt, lp, lg, left, lmask);
       set_item();
     }
   };
@@ -218,10 +222,11 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
       uint32_t at = foff[i];
       if constexpr (G > 1)
         at += scales_first<B>(min(fsteps[buf] + fstep[i], steps - 1), blocks);
+      at &= fmask;
       load_scales<B, S, ZP, NST == 1>(p.scales + first, ZP ? p.zeros + first : nullptr, at, blocks,
                                       fetched[buf][i]);
     }
-    step_on(fj, ft, fp, fg, fleft);
+    step_on(fj, ft, fp, fg, fleft, fmask);
   };
   const auto put = [&](int buf) {
 #pragma unroll

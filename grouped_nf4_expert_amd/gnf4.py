@@ -159,14 +159,15 @@ _HERE = contextlib.nullcontext()
 def _same_device(first, **others):
     """Refuse host tensors and tensors that are not on `first`'s device (None
     is skipped); return a context in which that device is the current one."""
+    device = first.get_device()
     for name, t in others.items():
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != device:
             raise ValueError(f"{name} is on {t.device}, expected {first.device}")
-    if not first.is_cuda:
+    if device < 0:
         raise Gnf4Error(GNF4_ERR_NOT_DEVICE_PTR, "host tensor")
-    if first.get_device() == torch.cuda.current_device():
+    if device == torch.cuda.current_device():
         return _HERE  # entering torch.cuda.device costs a microsecond
-    return torch.cuda.device(first.device)
+    return torch.cuda.device(device)
 
 
 # ------------------------------------------------------------------- pack
@@ -480,9 +481,11 @@ def int4_linear(x, packed, scales, zeros=None, bias=None, out=None):
     with _same_device(x, packed=packed, scales=scales, zeros=zeros, bias=bias, out=out):
         if out is None:
             out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-        _check(library().gnf4_int4_linear(_ptr(x), M, _ptr(packed), _ptr(scales), sdt,
-                                          _ptr(zeros), K // groups, N, K, _ptr(bias), _ptr(out),
-                                          _stream()), "gnf4_int4_linear")
+        status = library().gnf4_int4_linear(
+            x.data_ptr(), M, packed.data_ptr(), scales.data_ptr(), sdt,
+            None if zeros is None else zeros.data_ptr(), K // groups, N, K,
+            None if bias is None else bias.data_ptr(), out.data_ptr(), _stream())
+        _check(status, "gnf4_int4_linear")
     return out
 
 
