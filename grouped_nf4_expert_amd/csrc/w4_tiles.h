@@ -12,7 +12,12 @@
 //    read per item, they cost the address units four times what the weights
 //    do;
 //  * each wavefront loads weights ahead, across items and barriers: a CU must
-//    keep tens of kilobytes in flight to draw its share of the HBM stream.
+//    keep tens of kilobytes in flight to draw its share of the HBM stream.  (More
+//    is not better: five and seven steps of two tiles ahead instead of two and
+//    three cost 5-9% of calls with a few items per team.)
+// Measured on the gate_up of 64 experts' 4096 x 2048 matrices (49 us then): without
+// the products 45, without scales 46, without both 42, without the ends of items
+// 45: no single part bounds it but the stream and its start.
 #pragma once
 
 #include "w4_mfma.h"
@@ -165,9 +170,12 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
     return (size_t)read_entry(ev).e * p.expert_rows + (size_t)p.first_row(tile);
   };
   const auto set_item = [&]() { cbase = p.codes + first_row(lj, lt + lg) * (size_t)kb; };
-  // one item (of a pass) on; past the last group the last one again, where a
-  // zero mask leaves one line to read (whole tiles cost two of ten rounds)
-  const auto step_on = [&](int& j, int& t, int& pass, int& item, int& rest, uint32_t& mask) {
+  // One item (of a pass) on; past the last group the last one again.  A team with
+  // a group less than its workgroup's other teams stores that one twice, so its
+  // loads stay whole; past the last round, where nothing is used, a zero mask
+  // leaves one line to read (1 token over 64 experts 27.7 -> 25.2 us).
+  const auto step_on = [&](int& j, int& t, int& pass, int& item, int& rest, int& more,
+                           uint32_t& mask) {
     if constexpr (G > 1) {
       if (++item < G) return;
       item = 0;
@@ -181,18 +189,21 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
         t = 0;
         j = uniform(j + 1);
       }
-    } else {
-      mask = 0u;
     }
+    if (more > 0)
+      --more;
+    else
+      mask = 0u;
   };
   uint32_t lmask = ~0u, fmask = ~0u;
+  int lmore = rounds - 1, fmore = rounds - 1;
   const auto load = [&](u32x4 (&w)[U], int i) {
     const int c = min((lp * wk + kw) * NST + i, steps - 1);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       w[u] = load_codes(cbase, c, coff[u], g, kb, lmask);
     if (i == NST - 1) {
-      step_on(lj, lt, lp, lg, left, lmask);
+      step_on(lj, lt, lp, lg, left, lmore, lmask);
       set_item();
     }
   };
@@ -226,7 +237,7 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
       load_scales<B, S, ZP, NST == 1>(p.scales + first, ZP ? p.zeros + first : nullptr, at, blocks,
                                       fetched[buf][i]);
     }
-    step_on(fj, ft, fp, fg, fleft, fmask);
+    step_on(fj, ft, fp, fg, fleft, fmore, fmask);
   };
   const auto put = [&](int buf) {
 #pragma unroll

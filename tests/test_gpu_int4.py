@@ -169,6 +169,25 @@ def test_linear_row_lengths(steps, N):
         test_linear_parity(1 + steps % 16, N, K, group, zp, "bf16" if steps % 2 else "f32")
 
 
+@pytest.mark.parametrize("N", [33000, 49990, 66001, 68033, 70017, 90050, 131201])
+@pytest.mark.parametrize("K", [64, 128, 256, 512])
+def test_linear_teams_of_unequal_shares(N, K):
+    """Items that do not divide among the teams of a workgroup (the bar above,
+    worked out in 64 bits on the GPU)."""
+    rng = np.random.default_rng(N + K)
+    packed, scales, _ = _weights(rng, N, K, 64, False, "f32")
+    q = torch.stack([packed >> 4, packed & 15], 2).view(N, K).double() - 8
+    w = (q.view(N, K // 64, 64) * scales.double()[..., None]).view(N, K)
+    for M in (1, 5):
+        note(f"int4_linear {M}x{N}x{K}")
+        x = bf16_dev(rng.standard_normal((M, K)))
+        y = gnf4.int4_linear(x, packed, scales).double()
+        o = x.double() @ w.t().contiguous()
+        mag = x.double().abs() @ w.t().contiguous().abs()
+        bad = (y - o).abs() > 2.0 ** -8 * o.abs() + K * 2.0 ** -23 * mag
+        assert not bad.any(), f"{int(bad.sum())} outside, first {bad.nonzero()[0].tolist()}"
+
+
 def test_linear_rows_do_not_depend_on_each_other():
     """A row keeps its bits whatever the other rows hold, infinities and NaN
     among them (rows of one matrix-core tile)."""
@@ -272,3 +291,6 @@ def test_refusals_on_the_gpu():
     off = torch.zeros(2 * 128 + 1, dtype=torch.bfloat16, device=DEV)[1:].view(2, 128)
     with pytest.raises(gnf4.Gnf4Error, match="invalid argument"):   # misaligned rows
         gnf4.int4_linear(off, p, s)
+    sq = torch.ones((128, 1), device=DEV)
+    with pytest.raises(gnf4.Gnf4Error, match="invalid argument"):   # y over x
+        gnf4.int4_linear(x, torch.zeros((128, 64), dtype=torch.uint8, device=DEV), sq, out=x)

@@ -141,6 +141,18 @@ def test_many_experts_and_picks(T, E, top_k):
     run_case(T, E, top_k, 64, 64, "nf4_bf16", residual=False)
 
 
+@pytest.mark.parametrize("fmt", ["nf4", "nf4_bf16", "mxfp4"])
+@pytest.mark.parametrize("T,H,I", [(11, 2112, 64), (13, 1728, 128), (17, 1344, 64), (7, 3264, 192)])
+def test_items_that_do_not_divide_among_teams(fmt, T, H, I):
+    """Every token on three experts of its own; some teams of a workgroup have
+    an item less than others."""
+    rng = np.random.default_rng(T)
+    logits = rng.standard_normal((T, 3 * T)).astype(np.float32)
+    for t in range(T):
+        logits[t, 3 * t:3 * t + 3] += 20.0
+    run_case(T, 3 * T, 3, H, I, fmt, False, logits=logits)
+
+
 @pytest.mark.parametrize("T", [16, 40, 64])
 def test_every_token_on_one_expert(T):
     """Groups of T rows (several matrix-core tiles) beside groups of none."""
