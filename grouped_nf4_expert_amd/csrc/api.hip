@@ -813,6 +813,7 @@ gnf4_status gnf4_int4_linear(const uint16_t* x, int64_t M, const uint8_t* packed
     if (!is_device_ptr(p)) return GNF4_ERR_NOT_DEVICE_PTR;
   if ((zeros && !is_device_ptr(zeros)) || (bias && !is_device_ptr(bias)))
     return GNF4_ERR_NOT_DEVICE_PTR;
+  if (x < y + M * N && y < x + M * K) return GNF4_ERR_INVALID_ARG;  // rows are read until the end
   Int4LinearArgs a;
   a.x = x;
   a.packed = packed;

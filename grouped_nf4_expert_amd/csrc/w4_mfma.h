@@ -44,16 +44,11 @@ typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 enum class W4 { kNf4, kMx4, kInt4 };
 
 constexpr int kStep = 128;          // K per step
 constexpr int kLutBytes = 64 * 1024;
-
-__device__ __forceinline__ int lane_id() {
-  return (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
-}
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, (half2v{(_Float16)lo, (_Float16)hi}));
@@ -70,7 +65,6 @@ __device__ __forceinline__ float e8m0_f32(uint32_t s) {
 
 __device__ __forceinline__ float scale_f32(float s) { return s; }
 __device__ __forceinline__ float scale_f32(uint16_t s) { return bf16_to_f32(s); }
-__device__ __forceinline__ float scale_f32(uint8_t s) { return e8m0_f32(s); }
 
 // Byte address of the i-th 4-byte word kept in the table rows' second halves.
 __device__ __forceinline__ int lds_half(int i) { return (i >> 5) * 256 + 128 + (i & 31) * 4; }

@@ -360,7 +360,7 @@ gnf4_status gnf4_int4_pack(const void* w, int32_t w_dtype, int64_t N, int64_t K,
  *   scales  [N, K/group] fp32 or bf16 bits (`scale_dtype`)
  *   zeros   [N, K/group] uint8 zero points 0..15, or NULL: every one is 8
  *   bias    [N] bf16 bits, or NULL
- *   y       [M, N] bf16 bits out
+ *   y       [M, N] bf16 bits out; must not overlap x (refused)
  *
  * Products of activations and codes are exact; a group's sum and the sums over
  * groups are fp32, y is rounded once.  Any M (one row up to a prompt's chunk)
