@@ -143,7 +143,7 @@ static size_t dtype_bytes(int32_t d) {
 static bool valid_int4_group(int32_t group, int64_t K) {
   return (group == 32 || group == 64 || group == 128) && K > 0 && K % group == 0;
 }
-// rows of one int4 linear call: 64 per workgroup along the grid's y
+// the widest int4 linear call
 constexpr int64_t kInt4MaxRows = (int64_t)1 << 20;
 constexpr int64_t kInt4MaxK = (int64_t)1 << 27;  // 32-bit offsets over 32 rows
 

@@ -441,14 +441,13 @@ def int4_pack(w, group=128, zero_points=False, scale_dtype=torch.bfloat16):
     K = w.shape[-1]
     rows = w.numel() // max(K, 1)
     with _same_device(w):
-        packed = torch.empty(w.shape[:-1] + (K // 2,), dtype=torch.uint8, device=w.device)
-        scales = torch.empty(w.shape[:-1] + (K // group,), dtype=scale_dtype, device=w.device)
-        zeros = None
-        if zero_points:
-            zeros = torch.empty(scales.shape, dtype=torch.uint8, device=w.device)
-        _check(library().gnf4_int4_pack(_ptr(w), _GNF4_DTYPES[w.dtype], rows, K, group,
-                                        _ptr(packed), _ptr(scales), sdt, _ptr(zeros), _stream()),
-               "gnf4_int4_pack")
+        packed = w.new_empty(w.shape[:-1] + (K // 2,), dtype=torch.uint8)
+        scales = w.new_empty(w.shape[:-1] + (K // group,), dtype=scale_dtype)
+        zeros = w.new_empty(scales.shape, dtype=torch.uint8) if zero_points else None
+        status = library().gnf4_int4_pack(
+            w.data_ptr(), _GNF4_DTYPES[w.dtype], rows, K, group, packed.data_ptr(),
+            scales.data_ptr(), sdt, None if zeros is None else zeros.data_ptr(), _stream())
+        _check(status, "gnf4_int4_pack")
     return packed, scales, zeros
 
 
@@ -480,7 +479,7 @@ def int4_linear(x, packed, scales, zeros=None, bias=None, out=None):
             raise ValueError("out must be [M, N]")
     with _same_device(x, packed=packed, scales=scales, zeros=zeros, bias=bias, out=out):
         if out is None:
-            out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+            out = x.new_empty((M, N))
         status = library().gnf4_int4_linear(
             x.data_ptr(), M, packed.data_ptr(), scales.data_ptr(), sdt,
             None if zeros is None else zeros.data_ptr(), K // groups, N, K,
