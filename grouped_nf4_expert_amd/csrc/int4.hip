@@ -119,7 +119,7 @@ void launch_pack_s(const Int4PackArgs& a, unsigned grid, hipStream_t stream) {
 // w4_tiles.h runs over one entry (the rows) and the matrix's tiles of 16 U rows.
 // 1 x 65537 x 8192 takes 55 us, 5.0 TB/s.  Matrices of a few megabytes are bound
 // by the chain of a launch (activations and scales, first weights, sums): 1 x
-// 2048 x 2048 5.0 us, 13 x 4096 x 7168 14 us.
+// 2048 x 2048 5.0 us, 13 x 4096 x 7168 13 us.
 
 template <typename S, int U>
 struct Rows {
@@ -170,7 +170,8 @@ template <int B, typename S, bool ZP, int U>
 void launch_rows_u(const Int4LinearArgs& a, const Launch& l, hipStream_t stream) {
   if constexpr (U == 1) {
     if (l.group > 1) return launch_rows_n<B, S, ZP, 4, kGroup, U>(a, l, stream);
-    if (l.nst > 6) return launch_rows_n<B, S, ZP, 8, 1, U>(a, l, stream);
+    if (l.nst > 7) return launch_rows_n<B, S, ZP, 8, 1, U>(a, l, stream);
+    if (l.nst > 6) return launch_rows_n<B, S, ZP, 7, 1, U>(a, l, stream);
   }
   if (l.nst == 1)
     launch_rows_n<B, S, ZP, 1, 1, U>(a, l, stream);

@@ -15,7 +15,7 @@
 // Few tokens wait for the chain of the launches: 1 token, 8 of 64 experts of 2048
 // x 1024 (28 MB), 25 us, of which each launch costs about 4 before its weights
 // stream.  Many experts are bound by the weight stream: 16 tokens over 256 experts
-// of 7168 x 2048 (2.5 GB) 600 us, 4.2 TB/s from cold caches; 64 tokens over 64
+// of 7168 x 2048 (2.5 GB) 577 us, 4.4 TB/s from cold caches; 64 tokens over 64
 // experts of 2048 x 1024 (227 MB) 78 us, 2.9 TB/s.
 
 #include <limits.h>
@@ -403,6 +403,8 @@ void project(const MoeLayerArgs& a, int experts, int max_entries, hipStream_t st
     const Launch l = plan_launch(experts, max_entries, cols / 16, K, 8);
     if (l.nst <= 6)
       launch_projection<F, B, S, kDown, 6, 1>(a, l, max_entries, stream);
+    else if (l.nst == 7)
+      launch_projection<F, B, S, kDown, 7, 1>(a, l, max_entries, stream);
     else
       launch_projection<F, B, S, kDown, 8, 1>(a, l, max_entries, stream);
   }

@@ -134,7 +134,8 @@ __device__ __forceinline__ void expert_tiles(const P& p, const ItemGrid ig, int 
                                              char* lut, char* slds) {
   typedef ScaleWord<B, S, ZP> Scale;
   // steps held or in flight: 2 KB each with two tiles, 1 KB with one
-  constexpr int kBufs = U == 1 && NST > 2 ? (NST % 3 == 0 ? 6 : 8) : NST == 3 ? 3 : 4;
+  constexpr int kBufs =
+      U == 1 && NST > 2 ? (NST % 3 == 0 ? 6 : NST == 7 ? 7 : 8) : NST == 3 ? 3 : 4;
   constexpr int kAhead = kBufs - 1;
   constexpr int kUnroll = G > 1 ? G : NST == 1 ? 4 : 2;  // items per turn of the loop
   static_assert(NST * kUnroll % kBufs == 0 && kUnroll % 2 == 0,

@@ -130,7 +130,7 @@ def test_shapes(fmt, T, E, top_k, H, I):
     (2, 4, 2, 4160, 64), (9, 3, 2, 6208, 128), (1, 3, 2, 8192, 64), (20, 3, 2, 7168, 64),
     (3, 4, 2, 64, 4160), (1, 3, 2, 128, 8192), (18, 2, 1, 64, 6144), (1, 2, 1, 5120, 5120)])
 def test_long_rows(fmt, T, E, top_k, H, I):
-    """Rows past 4096: items of one column tile, six or eight steps of K per
+    """Rows past 4096: items of one column tile, six to eight steps of K per
     wavefront."""
     run_case(T, E, top_k, H, I, fmt, residual=T % 2 == 1)
 
